@@ -57,7 +57,8 @@ typedef enum {
     WLQ_ERR_NONFINITE = 5,   /* a weight was NaN or +-Inf (device-detected) */
     WLQ_ERR_WORKSPACE = 6,   /* workspace missing or smaller than required */
     WLQ_ERR_TIMEOUT = 7,     /* a bounded device wait ran out              */
-    WLQ_ERR_CUDA = 8         /* a CUDA runtime / driver call failed        */
+    WLQ_ERR_CUDA = 8,        /* a CUDA runtime / driver call failed        */
+    WLQ_ERR_INDEX = 9        /* an offset, length or page out of range (device-detected) */
 } wlq_status;
 
 typedef enum { WLQ_OUT_BF16 = 0, WLQ_OUT_F32 = 1 } wlq_out_dtype;
@@ -295,7 +296,8 @@ wlq_status wlq_lowrank_residual(const float* W, const void* L1, const void* L2, 
 
 /*
  * Synchronise `stream`, then read and clear this device's error word:
- * WLQ_OK, WLQ_ERR_NONFINITE or WLQ_ERR_TIMEOUT (or WLQ_ERR_CUDA).
+ * WLQ_OK, WLQ_ERR_NONFINITE, WLQ_ERR_TIMEOUT or WLQ_ERR_INDEX (or
+ * WLQ_ERR_CUDA).
  * The error path follows "Nunchaku Lite", section "hardware and precision
  * support": the quantizer checks the GPU's compute capability when it loads
  * and raises a clear error on a mismatch.  Here every call returns
@@ -366,6 +368,113 @@ size_t wlq_w4a4_workspace(int64_t M, int64_t N, int64_t K, int r);
 wlq_status wlq_w4a4_linear(const void* x, int64_t M, const void* wq, const void* ws, const float* wg,
                            int64_t N, int64_t K, const void* bias, const void* L1, const void* L2, int r,
                            void* y, int y_dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Norms of queries and keys for each head with the position rotation, one
+ * pass ("Joy-face_change_optimized" model card, fused ops: QK-norm + 3D
+ * RoPE).  For each token t and head, x the head's head_dim values:
+ *   n_d = x_d w_d / sqrt(mean_d x_d^2 + eps)          (weight NULL: n = x)
+ *   each rotated pair (a, b), i = its number, angle = positions[t][axis(i)]
+ *   * inv_freq[i]:   a' = a cos - b sin,  b' = a sin + b cos
+ * and the result is the bf16 value nearest to the real one (one rounding).
+ * Pairs: interleaved != 0: inputs (2 i, 2 i + 1); 0: (i, i + rotary_dim / 2).
+ * Inputs from rotary_dim on are normed but not rotated.  sections[a] pairs
+ * turn by axis a, in order (1 axis: text; 2 or 3: height, width / time,
+ * height, width of images and video).
+ * q, k   : bf16, token t's head h at t * stride + h * head_dim (so views of a
+ *          fused projection need no copy); either may be NULL with 0 heads
+ * weights: bf16 [head_dim] or NULL
+ * positions: int32 [tokens, axes] or NULL (no rotation); any values
+ * inv_freq : fp32 [rotary_dim / 2]; sections: HOST int32 [axes]
+ * q_out, k_out: bf16 with their own token strides; may be q and k themselves
+ *          (same stride), otherwise they must not overlap any input
+ * head_dim 64 or 128; rotary_dim a multiple of 16, at most head_dim; axes
+ * 1..4; strides multiples of 8 and at least heads * head_dim; q, k, q_out and
+ * k_out 16-byte aligned.  tokens == 0 is a no-op.
+ */
+wlq_status wlq_qk_norm_rope(const void* q, int64_t q_stride, int q_heads, const void* k, int64_t k_stride, int k_heads,
+                            int64_t tokens, int head_dim, const void* q_weight, const void* k_weight, double eps,
+                            const int32_t* positions, int axes, const float* inv_freq, int rotary_dim,
+                            const int32_t* sections, int interleaved, void* q_out, int64_t q_out_stride, void* k_out,
+                            int64_t k_out_stride, void* stream);
+
+/*
+ * The paged 4-bit KV cache (the card's KV-dtype setting, section 1, at 4 bits
+ * with scales for groups of each token and head).  Four device arrays:
+ *   codes  k, v : uint8 [num_pages, heads, page_size, head_dim / 2]
+ *   scales k, v : fp16  [num_pages, heads, page_size, head_dim / group]
+ * A group of `group` inputs holds s = fp16(max |x| / 7) and codes
+ * q = clamp(round_half_even(x / s), -7, 7), as wlq_quantize_ex(bits 4, fp16
+ * scales); 32-bit words of 8 inputs store q + 8, input t at nibble t / 2
+ * (t even) or 4 + t / 2 (t odd).
+ * page_size 16, 32, 64, 128 or 256; group 32, 64 or 128, at most head_dim;
+ * head_dim 64 or 128; code arrays 16-byte aligned, scale arrays 16-byte aligned.
+ *
+ * A call's sequences: sequence b owns tokens cu_seqlens[b] .. cu_seqlens[b+1]
+ * of the token-indexed tensors (`tokens` rows in all; rows that no sequence
+ * owns are neither read nor written), which are the LAST of its kv_lens[b]
+ * cached tokens; cached token j lies on page block_table[b][j / page_size].
+ * cu_seqlens int32 [batch + 1], kv_lens int32 [batch], block_table int32
+ * [batch, table_width] (entries past a sequence's pages are not read), all on
+ * the device.  max_q: an upper bound of the sequences' token counts (host).
+ * Offsets, lengths or pages out of range (a sequence of more than max_q tokens
+ * or fewer cached ones than tokens, a page outside the pool or the table) set
+ * WLQ_ERR_INDEX in the device error word; the tokens concerned are skipped.
+ *
+ * wlq_kv4_append: keys normed and rotated as by wlq_qk_norm_rope (k_weight,
+ * positions NULL: neither; same bits as that call), values as they are, both
+ * rounded to 4 bits and written to their places.  k, v: bf16 with token
+ * strides.  A value beyond 65280 in magnitude, an infinity or a NaN sets
+ * WLQ_ERR_NONFINITE; its group gets scale 0 and codes 0.  Pages that one call
+ * writes must belong to one sequence.  batch * max_q < 2^31.
+ */
+wlq_status wlq_kv4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t tokens, int heads,
+                          int head_dim, const void* k_weight, double eps, const int32_t* positions, int axes,
+                          const float* inv_freq, int rotary_dim, const int32_t* sections, int interleaved,
+                          const int32_t* cu_seqlens, const int32_t* kv_lens, int batch, int max_q,
+                          const int32_t* block_table, int64_t table_width, void* k_codes, void* k_scales, void* v_codes,
+                          void* v_scales, int64_t num_pages, int page_size, int group, void* stream);
+
+/*
+ * The cached rows of the call's tokens back as bf16 (code * scale, rounded
+ * once): k_out, v_out bf16 [tokens, heads, head_dim], 16-byte aligned.  With
+ * as many tokens as cached ones this reads a whole sequence.
+ */
+wlq_status wlq_kv4_read(const int32_t* cu_seqlens, const int32_t* kv_lens, int batch, int max_q,
+                        const int32_t* block_table, int64_t table_width, const void* k_codes, const void* k_scales,
+                        const void* v_codes, const void* v_scales, int64_t num_pages, int page_size, int group,
+                        int64_t tokens, int heads, int head_dim, void* k_out, void* v_out, void* stream);
+
+/*
+ * Attention over the paged 4-bit cache, after the call's own tokens were
+ * appended: query i of sequence b (n queries) stands at position
+ * p = kv_lens[b] - n + i, and for each head
+ *   out = softmax_j(scale q . k_j) v_j    over the cached tokens j it sees:
+ * all of them (causal 0), j <= p (causal 1), p - window < j <= p (causal 1,
+ * window > 0).  Query head h reads cache head h / (q_heads / kv_heads).
+ * A query that sees nothing gets zeros (lse -inf).
+ * q   : bf16, token strides as above; out: bf16 [tokens, q_heads, head_dim]
+ * lse : fp32 [tokens, q_heads], log sum_j exp(scale q . k_j), or NULL
+ * max_kv: an upper bound of kv_lens (host).  It only plans how long caches are
+ *         split; any value gives right results.  The tokens of a page out of
+ *         range count as not seen (WLQ_ERR_INDEX is set).
+ * scale: finite, any sign.  Scores, softmax statistics and sums are fp32; keys,
+ * values and weights enter the tensor cores as fp16 (code * scale and
+ * exp(. - max), each rounded once), queries as fp16 of q 2^e with one power
+ * of two per row (exact unless a value lies 2^-29 below its row's largest).
+ * Results are bitwise reproducible run to run.
+ * workspace: wlq_kv4_attention_workspace() bytes (0: none needed), 16-byte
+ * aligned, contents need no initialisation; calls that may overlap on the GPU
+ * must not share one.
+ */
+size_t wlq_kv4_attention_workspace(int64_t tokens, int batch, int max_q, int64_t max_kv, int q_heads, int kv_heads,
+                                   int head_dim);
+wlq_status wlq_kv4_attention(const void* q, int64_t q_stride, int64_t tokens, int q_heads, int kv_heads, int head_dim,
+                             const int32_t* cu_seqlens, const int32_t* kv_lens, int batch, int max_q, int64_t max_kv,
+                             const int32_t* block_table, int64_t table_width, const void* k_codes, const void* k_scales,
+                             const void* v_codes, const void* v_scales, int64_t num_pages, int page_size, int group,
+                             float scale, int causal, int window, void* out, float* lse, void* workspace,
+                             size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

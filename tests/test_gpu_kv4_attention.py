@@ -1,0 +1,257 @@
+"""kv4_attention against the 64-bit form (tests/attention_ref.py).
+
+Bounds, from the roundings the header names.  Keys, values and weights enter
+the products as fp16 (2^-11 relative each), scores and sums are fp32, the
+output is rounded to bf16 (2^-8).  With E the largest possible score error of a
+query, max_j scale sum_d |q_d k_jd| (2^-11 + 2^-20), A = sum_j p_j |v_j| and
+B = 2^-25 sum_j |v_j|:
+    |out - ref| <= 2^-8 |ref| + (A (2 E + 2 * 2^-11 + 2^-16) + B) (1 + 2^-8),
+    |lse - ref| <= E + 2^-16 max(1, |ref|)
+(a weight's relative error is at most e^(2 E) - 1 after normalising; a weight
+below 2^-14 of the running maximum's is an fp16 subnormal, whose half step is
+2^-25, and the sum the weights are divided by is at least 1: B; 2^-16
+covers ex2.approx and the fp32 sums of at most 2^16 terms' worth of rounding).
+For random values the errors average out: the 2-norm error stays below 2^-8
+of the result's (2^-8 / sqrt 3 from the output's rounding, 2^-11 each from the
+other roundings, added in squares)."""
+import numpy as np
+import pytest
+import torch
+
+from tests import attention_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def wlq():
+    import weight_only_quantized_rtn_b200 as m
+    return m
+
+
+def make(seed, q_lens, kv_lens, hk, share, D, group, page, extra_pages=3, pool=None, tail=0):
+    """Random cache on scattered pages; places no sequence owns hold NaN scales, rows of no sequence NaN queries."""
+    g = torch.Generator().manual_seed(seed)
+    per = max(1, max(-(-k // page) for k in kv_lens))
+    pages = pool or len(kv_lens) * per + extra_pages
+    table = torch.randperm(pages, generator=g)[: len(kv_lens) * per].reshape(len(kv_lens), per).to(torch.int32)
+    if pool:  # the last pages of a large pool
+        table = (pool - 1 - torch.randperm(len(kv_lens) * per, generator=g)).reshape(len(kv_lens), per).to(torch.int32)
+    cu = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+    T = int(cu[-1]) + tail
+    m = wlq()
+    cache = m.Kv4Cache(pages, hk, page, D, group)
+    if not pool:
+        for t in (cache[1], cache[3]):
+            t.fill_(float("nan"))
+        for t in (cache[0], cache[2]):
+            t.copy_(torch.randint(0, 256, t.shape, generator=g, dtype=torch.uint8))
+    for b, kv in enumerate(kv_lens):
+        for p in range(-(-kv // page)):
+            n, pg = min(page, kv - p * page), int(table[b, p])
+            for ci, spread in ((0, 2.0), (2, 1.0)):
+                x = torch.randn(hk, n, D, generator=g) * torch.exp(0.5 * spread * torch.randn(hk, n, 1, generator=g))
+                q, s = ref.quantize4(ref.f64(x.bfloat16()), group)
+                cache[ci][pg, :, :n] = torch.from_numpy(ref.pack4(q)).cuda()
+                cache[ci + 1][pg, :, :n] = torch.from_numpy(s.astype(np.float16)).cuda()
+    q = torch.randn(T, hk * share, D, generator=g).bfloat16()
+    q[int(cu[-1]):] = float("nan")
+    return q.cuda(), cache, cu, np.array(kv_lens, dtype=np.int32), table.numpy()
+
+
+def bounds(q, cache, cu, kv_lens, table, hk, scale):
+    """E [T, Hq] and B [T, Hq, D]: see the module's text."""
+    T, Hq, D = q.shape
+    E, B = np.zeros((T, Hq)), np.zeros((T, Hq, D))
+    P = cache[0].shape[2]
+    for b in range(len(kv_lens)):
+        pages = table[b][: -(-kv_lens[b] // P)]
+        for h in range(Hq):
+            if kv_lens[b]:
+                k = np.nan_to_num(np.abs(ref.cache_values(cache, "k", pages, h // (Hq // hk), kv_lens[b])))
+                E[cu[b]:cu[b + 1], h] = (np.abs(q[cu[b]:cu[b + 1], h]) @ k.T).max(-1) * abs(scale) * (2.0 ** -11 + 2.0 ** -20)
+                v = np.nan_to_num(np.abs(ref.cache_values(cache, "v", pages, h // (Hq // hk), kv_lens[b])))
+                B[cu[b]:cu[b + 1], h] = v.sum(0) * 2.0 ** -25
+    return E, B
+
+
+def check(m, q, cache, cu, kv, table, hk, causal, window, scale=None, max_q=None, max_kv=None, ws=None, random=True):
+    T, Hq, D = q.shape
+    dev = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in (cu, kv, table)]
+    out = torch.full((T, Hq, D), -7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, Hq), -7.0, device="cuda")
+    max_q = int(max(np.diff(cu))) if max_q is None else max_q
+    max_kv = int(max(kv)) if max_kv is None else max_kv
+    m.kv4_attention(q, cache, *dev, max_q, max_kv, scale=scale, causal=causal, window=window, out=out, lse=lse, workspace=ws)
+    sc = D ** -0.5 if scale is None else scale
+    n = int(cu[-1])
+    qn = ref.f64(q)[:n]
+    want, want_lse = ref.attention(qn, cache, cu, kv, table, hk, sc, causal, window)
+    E, B = bounds(qn, cache, cu, kv, table, hk, sc)
+    A = ref_abs(qn, cache, cu, kv, table, hk, sc, causal, window)
+    got, got_lse = ref.f64(out), ref.f64(lse)
+    assert (got[n:] == -7).all() and (got_lse[n:] == -7).all()  # rows of no sequence
+    got, got_lse = got[:n], got_lse[:n]
+    tol = 2.0 ** -8 * np.abs(want) + (A * (np.expm1(2 * E) + 2.0 ** -10 + 2.0 ** -16)[..., None] + B) * (1 + 2.0 ** -8)
+    err = np.abs(got - want)
+    assert (err <= tol).all(), "%r" % ((np.nanmax(err / tol), np.unravel_index(np.nanargmax(err / tol), err.shape)),)
+    none = np.isneginf(want_lse)
+    assert (np.isneginf(got_lse) == none).all() and (got[none] == 0).all()
+    el = np.abs(got_lse[~none] - want_lse[~none])
+    assert (el <= E[~none] + 2.0 ** -16 * np.maximum(1, np.abs(want_lse[~none]))).all()
+    if random and n * Hq >= 8:
+        assert np.linalg.norm(got - want) <= 2.0 ** -8 * np.linalg.norm(want)
+    return out, lse
+
+
+def ref_abs(q, cache, cu, kv, table, hk, sc, causal, window):
+    """sum_j p_j |v_j|: the reference with the values' magnitudes (codes mirrored to their absolute value)."""
+    D = q.shape[-1]
+    v = cache[2].cpu().numpy()
+    a = ref.pack4(np.abs(ref.unpack4(v, D)))
+    return ref.attention(q, (cache[0], cache[1], torch.from_numpy(a), cache[3]), cu, kv, table, hk, sc, causal, window)[0]
+
+
+@pytest.mark.parametrize("D,group,page", [(128, 32, 16), (128, 64, 64), (128, 128, 256), (64, 32, 32), (64, 64, 128)])
+@pytest.mark.parametrize("hk,share", [(1, 1), (2, 4), (3, 8), (1, 12), (2, 16)])
+def test_single_tokens(D, group, page, hk, share):
+    m = wlq()
+    kv = [1, 15, 16, 17, 33, 300]
+    a = make(hk * share + D, [1] * len(kv), kv, hk, share, D, group, page, tail=2)
+    check(m, *a, hk, True, 0)
+    m.check_status()
+
+
+@pytest.mark.parametrize("D,page", [(128, 16), (64, 64)])
+@pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 1), (True, 7), (True, 130), (True, 100000)])
+@pytest.mark.parametrize("share", [1, 4])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1], [1]), ([5, 0, 1, 20], [5, 0, 90, 44]), ([37, 129], [200, 129]), ([3, 1, 2], [3, 700, 260])])
+def test_chunks(D, page, causal, window, share, q_lens, kv_lens):
+    m = wlq()
+    a = make(sum(q_lens) + share, q_lens, kv_lens, 2, share, D, 32, page, tail=1)
+    check(m, *a, 2, causal, window)
+    m.check_status()
+
+
+@pytest.mark.parametrize("kv,window", [(5000, 0), (20011, 0), (20011, 600)])
+def test_long_caches_are_split(kv, window):
+    m = wlq()
+    a = make(kv, [1, 1], [kv, 40], 1, 4, 128, 64, 128)
+    assert m.kv4_attention_workspace(2, 2, 1, kv, 4, 1, 128) > 0
+    out, lse = check(m, *a, 1, True, window)
+    again, _ = check(m, *a, 1, True, window, ws=torch.full((m.kv4_attention_workspace(2, 2, 1, kv, 4, 1, 128),), 255, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(out, again)  # reproducible, whatever the workspace held
+    check(m, *a, 1, True, window, max_kv=1)      # wrong bounds of the lengths cost speed, not results
+    check(m, *a, 1, True, window, max_kv=1 << 20)
+    check(m, *a, 1, True, window, max_q=3)
+    m.check_status()
+
+
+def test_scores_that_grow_move_the_maximum():
+    """Keys whose scores climb by far more than the lazy maximum's 2^8, then fall; the largest last, first and in between."""
+    m = wlq()
+    D, n = 64, 257
+    for order in (np.arange(n), np.arange(n)[::-1].copy(), np.abs(np.arange(n) - 128)):
+        q, cache, cu, kv, table = make(11, [3], [n], 1, 2, D, 32, 16)
+        pages = table[0]
+        for j in range(n):
+            s = np.float16(0.02 * (order[j] + 1))
+            cache[1][pages[j // 16], 0, j % 16] = torch.tensor(s)
+            cache[0][pages[j // 16], 0, j % 16] = torch.from_numpy(ref.pack4(np.full(D, 7, dtype=np.int8))).cuda()
+        q.abs_()
+        check(m, q, cache, cu, kv, table, 1, False, 0, scale=1.0, random=False)
+        check(m, q, cache, cu, kv, table, 1, False, 0, scale=-1.0, random=False)
+
+
+def test_scale_zero_and_wide_queries():
+    m = wlq()
+    a = make(3, [2, 9], [50, 9], 2, 4, 128, 64, 16)
+    check(m, *a, 2, True, 0, scale=0.0)
+    q = a[0].clone()
+    q[0, 0] *= 1e30     # large and tiny rows: their power of two is taken out and put back
+    q[1, 1] *= 1e-30
+    check(m, q, *a[1:], 2, True, 0, scale=1e-30, random=False)
+    q = a[0].clone()
+    q[:] = 0
+    check(m, q, *a[1:], 2, True, 0)
+
+
+def test_query_views_and_reproducible():
+    m = wlq()
+    q, cache, cu, kv, table = make(5, [4, 7], [60, 7], 2, 4, 128, 64, 16)
+    wide = torch.zeros(11, 3 * 8 * 128, dtype=torch.bfloat16, device="cuda")
+    wide[:, : 8 * 128] = q.reshape(11, -1)
+    dev = [torch.from_numpy(x).cuda() for x in (cu, kv, table)]
+    a = m.kv4_attention(q, cache, *dev, 7, 60)
+    b = m.kv4_attention(wide[:, : 8 * 128].view(11, 8, 128), cache, *dev, 7, 60)
+    assert torch.equal(a, b)
+
+
+def test_a_cache_beyond_four_gigabytes():
+    """Pages whose codes lie past 2^32 bytes."""
+    m = wlq()
+    pool = 70000
+    a = make(9, [1, 2], [130, 200], 8, 4, 128, 128, 128, pool=pool)
+    assert a[1][0].numel() > 1 << 32
+    check(m, *a, 8, True, 0)
+    m.check_status()
+
+
+def test_pages_out_of_range_count_as_not_seen():
+    m = wlq()
+    q, cache, cu, kv, table = make(6, [1, 1], [64, 40], 1, 2, 64, 32, 16)
+    table = table.copy()
+    table[0, 1] = -1
+    table[0, 2] = cache[0].shape[0]
+    table[1, :] = 1 << 30
+    check(m, q, cache, cu, kv, table, 1, True, 0, random=False)
+    assert m.get_status() == m.ERR_INDEX
+    # a table narrower than the sequence
+    check_table = torch.from_numpy(table[:, :1].copy()).cuda()
+    m.kv4_attention(q, cache, torch.from_numpy(cu).cuda(), torch.from_numpy(kv).cuda(), check_table, 1, 64)
+    assert m.get_status() == m.ERR_INDEX
+    m.check_status()
+
+
+def test_lengths_out_of_range_are_skipped():
+    m = wlq()
+    q, cache, cu, kv, table = make(6, [3, 2], [64, 40], 1, 2, 64, 32, 16)
+    for c, k, max_q in (([0, 3, 6], [64, 40], 3), ([0, 3, 5], [2, 40], 3), ([0, 3, 5], [64, 40], 2), ([-1, 3, 5], [64, 40], 4)):
+        out = torch.full_like(q, -7.0)
+        m.kv4_attention(q, cache, torch.tensor(c, dtype=torch.int32, device="cuda"), torch.tensor(k, dtype=torch.int32, device="cuda"),
+                        torch.from_numpy(table).cuda(), max_q, 64, out=out)
+        assert m.get_status() == m.ERR_INDEX
+        bad = [r for b in range(2) for r in range(max(c[b], 0), min(c[b + 1], 5))
+               if c[b] < 0 or c[b + 1] > 5 or k[b] < c[b + 1] - c[b] or c[b + 1] - c[b] > max_q]
+        assert bad and (out[bad] == -7).all()
+        good = [r for r in range(5) if r not in bad]
+        assert (out[good] != -7).any()
+
+
+def test_streams_and_graphs():
+    m = wlq()
+    q, cache, cu, kv, table = make(8, [1, 1], [3000, 500], 2, 4, 128, 64, 64)
+    dev = [torch.from_numpy(x).cuda() for x in (cu, kv, table)]
+    want = m.kv4_attention(q, cache, *dev, 1, 3000)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    torch.cuda.synchronize()
+    for s in (s1, s2):  # two calls at once, a workspace each
+        with torch.cuda.stream(s):
+            outs.append(m.kv4_attention(q, cache, *dev, 1, 3000))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        o1 = m.kv4_attention(q, cache, *dev, 1, 3000)
+    with torch.cuda.graph(g2):
+        o2 = m.kv4_attention(q, cache, *dev, 1, 3000)
+    q.copy_(q.flip(0))
+    want = m.kv4_attention(q, cache, *dev, 1, 3000)
+    for _ in range(2):
+        g1.replay()
+        g2.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o1, want) and torch.equal(o2, want)
+    dev[1].fill_(64)  # the lengths are read when the graph runs
+    g1.replay()
+    assert torch.equal(o1, m.kv4_attention(q, cache, *dev, 1, 3000))

@@ -16,7 +16,8 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libwlq.so")
 
-OK, ERR_INVALID_ARG, ERR_SHAPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_NONFINITE, ERR_WORKSPACE, ERR_TIMEOUT, ERR_CUDA = range(9)
+OK, ERR_INVALID_ARG, ERR_SHAPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_NONFINITE, ERR_WORKSPACE, ERR_TIMEOUT, ERR_CUDA, \
+    ERR_INDEX = range(10)
 OUT_BF16, OUT_F32 = 0, 1
 STATUS_NAMES = {
     OK: "WLQ_OK", ERR_INVALID_ARG: "WLQ_ERR_INVALID_ARG", ERR_SHAPE: "WLQ_ERR_SHAPE",
@@ -28,7 +29,7 @@ EXPORTS = ("wlq_quantize", "wlq_quantize_pack", "wlq_quantize_ex", "wlq_quantize
            "wlq_pack", "wlq_unpack", "wlq_linear_workspace", "wlq_linear", "wlq_linear_noalloc",
            "wlq_lowrank_workspace", "wlq_lowrank_split", "wlq_lowrank_residual", "wlq_nvfp4_scales_bytes",
            "wlq_nvfp4_quantize", "wlq_nvfp4_linear_workspace", "wlq_nvfp4_linear", "wlq_w4a4_workspace",
-           "wlq_w4a4_linear", "wlq_get_status",
+           "wlq_w4a4_linear", "wlq_qk_norm_rope", "wlq_kv4_append", "wlq_kv4_read", "wlq_kv4_attention", "wlq_get_status",
            "wlq_probe_wait_timeout", "wlq_set_grid_limit", "wlq_last_error", "wlq_version")
 
 if not os.path.exists(LIB_PATH):
@@ -36,6 +37,7 @@ if not os.path.exists(LIB_PATH):
 
 lib = ctypes.CDLL(LIB_PATH)
 _i64, _i32, _vp, _sz, _u64 = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint64
+_f64 = ctypes.c_double
 lib.wlq_quantize.argtypes = [_vp, _i64, _i64, _i32, _i32, _vp, _vp, _vp]
 lib.wlq_packed_bytes.argtypes = [_i64, _i64, _i32, _i32]
 lib.wlq_packed_bytes.restype = _sz
@@ -62,6 +64,16 @@ lib.wlq_nvfp4_linear.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, 
 lib.wlq_w4a4_workspace.argtypes = [_i64, _i64, _i64, _i32]
 lib.wlq_w4a4_workspace.restype = _sz
 lib.wlq_w4a4_linear.argtypes = [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _sz, _vp]
+lib.wlq_qk_norm_rope.argtypes = [_vp, _i64, _i32, _vp, _i64, _i32, _i64, _i32, _vp, _vp, _f64, _vp, _i32, _vp, _i32, _vp,
+                                 _i32, _vp, _i64, _vp, _i64, _vp]
+lib.wlq_kv4_append.argtypes = [_vp, _i64, _vp, _i64, _i64, _i32, _i32, _vp, _f64, _vp, _i32, _vp, _i32, _vp, _i32,
+                               _vp, _vp, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp]
+lib.wlq_kv4_read.argtypes = [_vp, _vp, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i64, _i32, _i32,
+                             _vp, _vp, _vp]
+lib.wlq_kv4_attention_workspace.argtypes = [_i64, _i32, _i32, _i64, _i32, _i32, _i32]
+lib.wlq_kv4_attention_workspace.restype = _sz
+lib.wlq_kv4_attention.argtypes = [_vp, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _i32, _i32, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
+                                  _i64, _i32, _i32, ctypes.c_float, _i32, _i32, _vp, _vp, _vp, _sz, _vp]
 lib.wlq_get_status.argtypes = [_vp]
 lib.wlq_probe_wait_timeout.argtypes = [_u64, _vp]
 lib.wlq_set_grid_limit.argtypes = [_i32]
@@ -70,7 +82,8 @@ lib.wlq_last_error.restype = ctypes.c_char_p
 lib.wlq_version.restype = ctypes.c_char_p
 for _f in ("wlq_quantize", "wlq_quantize_pack", "wlq_quantize_ex", "wlq_quantize_fp8", "wlq_pack", "wlq_unpack", "wlq_linear",
            "wlq_linear_noalloc", "wlq_lowrank_split", "wlq_lowrank_residual", "wlq_nvfp4_quantize", "wlq_nvfp4_linear",
-           "wlq_w4a4_linear", "wlq_get_status", "wlq_probe_wait_timeout"):
+           "wlq_w4a4_linear", "wlq_qk_norm_rope", "wlq_kv4_append", "wlq_kv4_read", "wlq_kv4_attention", "wlq_get_status",
+           "wlq_probe_wait_timeout"):
     getattr(lib, _f).restype = ctypes.c_int
 
 
@@ -295,6 +308,195 @@ def w4a4_linear_into(y, x, wq, ws, wg, N, K, bias=None, L1=None, L2=None, worksp
     _check(lib.wlq_w4a4_linear(_ptr(x), M, _ptr(wq), _ptr(ws), _ptr(wg), N, K, _ptr(bias), _ptr(L1), _ptr(L2), r,
                                _ptr(y), out, _ptr(workspace), ws_n, _stream(stream)))
     return y
+
+
+# ------------------------------------------------- the attention layer's steps
+class Kv4Cache(tuple):
+    """A paged 4-bit KV cache: the tensors (k_codes, k_scales, v_codes, v_scales),
+    codes uint8 [pages, heads, page_size, head_dim / 2], scales fp16 [pages,
+    heads, page_size, head_dim / group].  Any 4-tuple of such tensors serves."""
+
+    def __new__(cls, num_pages: int, heads: int, page_size: int, head_dim: int, group: int, device="cuda"):
+        shapes = ((head_dim // 2, torch.uint8), (head_dim // group, torch.float16)) * 2
+        return super().__new__(cls, (torch.zeros((num_pages, heads, page_size, n), dtype=t, device=device)
+                                     for n, t in shapes))
+
+
+def _want(ok: bool, what: str):
+    if not ok:
+        raise WlqError(ERR_INVALID_ARG, what)
+
+
+def _on(*tensors):
+    """Every tensor on the current CUDA device, where the launch goes."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != cur):
+            raise WlqError(ERR_INVALID_ARG, "tensors must be on the current CUDA device (cuda:%d)" % cur)
+
+
+def _head_rows(name: str, x, head_dim: int):
+    """(pointer, token stride, heads) of bf16 x [tokens, heads, head_dim], heads contiguous within a token."""
+    T, H, D = x.shape
+    st = x.stride()
+    _want(x.dtype == torch.bfloat16, name + " must be bf16")
+    _want(D == head_dim and (st[2] == 1 or D <= 1) and (st[1] == D or H <= 1), name + ": a token's heads must be contiguous")
+    return x.data_ptr(), st[0] if T > 1 else H * D, H
+
+
+def _weight(name: str, w, head_dim: int):
+    if w is None:
+        return None
+    _want(w.dtype == torch.bfloat16 and w.numel() == head_dim and w.is_contiguous(), name + " must be contiguous bf16 [head_dim]")
+    return w.data_ptr()
+
+
+_SECTIONS = {}
+
+
+def _rope(positions, inv_freq, sections, tokens: int):
+    """(positions, axes, inv_freq, rotary_dim, sections) for the C call."""
+    if positions is None:
+        return None, 0, None, 0, None
+    _want(inv_freq is not None, "positions need inv_freq")
+    _want(positions.dtype == torch.int32 and positions.is_contiguous(), "positions must be contiguous int32")
+    _want(inv_freq.dtype == torch.float32 and inv_freq.is_contiguous() and inv_freq.dim() == 1, "inv_freq must be contiguous fp32 [pairs]")
+    axes = positions.shape[1] if positions.dim() == 2 else 1
+    _want(positions.dim() in (1, 2) and positions.shape[0] == tokens, "positions must be [tokens] or [tokens, axes]")
+    pairs = inv_freq.shape[0]
+    sections = (pairs,) if sections is None else tuple(sections)
+    _want(len(sections) == axes, "one section for each axis")
+    arr = _SECTIONS.get(sections)
+    if arr is None:
+        arr = _SECTIONS[sections] = (ctypes.c_int32 * axes)(*sections)
+    return positions.data_ptr(), axes, inv_freq.data_ptr(), 2 * pairs, arr
+
+
+def qk_norm_rope(q, k, positions=None, inv_freq=None, sections=None, interleaved: bool = True, q_weight=None,
+                 k_weight=None, eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """Norm of each head's queries and keys (RMS, times the weight; none without a
+    weight) and rotation by the positions, one pass -> (q_out, k_out), bf16.
+
+    q [tokens, q_heads, head_dim] and k [tokens, k_heads, head_dim]: bf16,
+    token stride free (views of a fused projection); either may be None.
+    positions int32 [tokens] or [tokens, axes], inv_freq fp32 [rotary_dim / 2],
+    sections: the pairs that turn by each axis.  interleaved: pairs (2 i,
+    2 i + 1), else (i, i + rotary_dim / 2).  q_out / k_out may be q / k."""
+    some = q if q is not None else k
+    _want(some is not None, "q or k is needed")
+    T, _, D = some.shape
+    _on(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
+    qp = kp = qo = ko = None
+    qs = ks = qos = kos = hq = hk = 0
+    if q is not None:
+        qp, qs, hq = _head_rows("q", q, D)
+        if q_out is None:
+            q_out = torch.empty((T, hq, D), dtype=torch.bfloat16, device=q.device)
+        _want(q_out.shape == q.shape, "q_out must have q's shape")
+        qo, qos, _ = _head_rows("q_out", q_out, D)
+    if k is not None:
+        _want(k.shape[0] == T, "q and k need the same tokens")
+        kp, ks, hk = _head_rows("k", k, D)
+        if k_out is None:
+            k_out = torch.empty((T, hk, D), dtype=torch.bfloat16, device=k.device)
+        _want(k_out.shape == k.shape, "k_out must have k's shape")
+        ko, kos, _ = _head_rows("k_out", k_out, D)
+    _check(lib.wlq_qk_norm_rope(qp, qs, hq, kp, ks, hk, T, D, _weight("q_weight", q_weight, D),
+                                _weight("k_weight", k_weight, D), eps, *_rope(positions, inv_freq, sections, T),
+                                int(interleaved), qo, qos, ko, kos, _stream(stream)))
+    return q_out, k_out
+
+
+def _pool(cache):
+    """(pointers..., num_pages, page_size, group), heads, head_dim of a 4-bit cache."""
+    kc, ks, vc, vs = cache
+    pages, H, P, half = kc.shape
+    groups = ks.shape[-1]
+    _want(kc.dtype == torch.uint8 and vc.dtype == torch.uint8 and ks.dtype == torch.float16 and vs.dtype == torch.float16,
+          "cache: uint8 codes and fp16 scales")
+    _want(vc.shape == kc.shape and vs.shape == ks.shape and ks.shape[:3] == kc.shape[:3] and groups > 0,
+          "cache: the arrays' shapes do not match")
+    _want(kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous(), "cache: contiguous arrays")
+    return (kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages, P, 2 * half // groups), H, 2 * half
+
+
+def _batch(cu_seqlens, kv_lens, block_table, max_q: int):
+    _want(cu_seqlens.dtype == torch.int32 and kv_lens.dtype == torch.int32 and block_table.dtype == torch.int32,
+          "cu_seqlens, kv_lens and block_table must be int32")
+    n = kv_lens.numel()
+    _want(cu_seqlens.numel() == n + 1 and block_table.dim() == 2 and block_table.shape[0] == n,
+          "cu_seqlens [batch + 1], kv_lens [batch], block_table [batch, width]")
+    _want(cu_seqlens.is_contiguous() and kv_lens.is_contiguous() and block_table.is_contiguous(),
+          "cu_seqlens, kv_lens and block_table must be contiguous")
+    return cu_seqlens.data_ptr(), kv_lens.data_ptr(), n, int(max_q), block_table.data_ptr(), block_table.shape[1]
+
+
+def kv4_append(cache, k, v, cu_seqlens, kv_lens, block_table, max_q: int, positions=None, inv_freq=None, sections=None,
+               interleaved: bool = True, k_weight=None, eps: float = 1e-6, stream=None):
+    """Keys (normed and rotated as by qk_norm_rope) and values rounded to 4 bits
+    into the paged cache.  k, v: bf16 [tokens, heads, head_dim], token stride
+    free.  Sequence b's tokens cu_seqlens[b] .. cu_seqlens[b + 1] become the
+    last of its kv_lens[b] cached ones, on pages block_table[b]; max_q: an upper
+    bound of the sequences' token counts."""
+    ptrs, H, D = _pool(cache)
+    T = k.shape[0]
+    _want(v.shape == k.shape and k.shape[1] == H, "k and v must be [tokens, the cache's heads, head_dim]")
+    _on(k, v, *cache, cu_seqlens, kv_lens, block_table, positions, inv_freq, k_weight)
+    kp, kst, _ = _head_rows("k", k, D)
+    vp, vst, _ = _head_rows("v", v, D)
+    _check(lib.wlq_kv4_append(kp, kst, vp, vst, T, H, D, _weight("k_weight", k_weight, D), eps,
+                              *_rope(positions, inv_freq, sections, T), int(interleaved),
+                              *_batch(cu_seqlens, kv_lens, block_table, max_q), *ptrs, _stream(stream)))
+
+
+def kv4_read(cache, cu_seqlens, kv_lens, block_table, max_q: int, tokens: int, stream=None):
+    """The cached rows of the call's tokens as bf16 -> (k, v) [tokens, heads,
+    head_dim] (rows of no sequence stay uninitialised)."""
+    ptrs, H, D = _pool(cache)
+    _on(*cache, cu_seqlens, kv_lens, block_table)
+    k = torch.empty((tokens, H, D), dtype=torch.bfloat16, device=cache[0].device)
+    v = torch.empty_like(k)
+    _check(lib.wlq_kv4_read(*_batch(cu_seqlens, kv_lens, block_table, max_q), *ptrs, tokens, H, D, k.data_ptr(),
+                            v.data_ptr(), _stream(stream)))
+    return k, v
+
+
+def kv4_attention_workspace(tokens: int, batch: int, max_q: int, max_kv: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    """Workspace bytes of kv4_attention (0: none needed)."""
+    return int(lib.wlq_kv4_attention_workspace(tokens, batch, max_q, max_kv, q_heads, kv_heads, head_dim))
+
+
+def kv4_attention(q, cache, cu_seqlens, kv_lens, block_table, max_q: int, max_kv: int, scale=None, causal: bool = True,
+                  window: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """Attention of bf16 q [tokens, q_heads, head_dim] (token stride free) over the
+    paged 4-bit cache -> out, bf16 [tokens, q_heads, head_dim].
+
+    Sequence b's queries cu_seqlens[b] .. cu_seqlens[b + 1] are the last of its
+    kv_lens[b] cached tokens; causal queries see up to themselves, with a
+    window only the last `window` of those.  A query that sees nothing gets 0.
+    max_q, max_kv: upper bounds of the lengths.  scale: 1 / sqrt(head_dim) by
+    default.  lse: fp32 [tokens, q_heads] to be filled, or None.  Rows of no
+    sequence are left as they were (uninitialised without out).  workspace: of
+    kv4_attention_workspace bytes; allocated here if None."""
+    ptrs, H, D = _pool(cache)
+    T, Hq, Dq = q.shape
+    _want(Dq == D, "q needs the cache's head_dim")
+    _on(q, *cache, cu_seqlens, kv_lens, block_table, out, lse, workspace)
+    qp, qs, _ = _head_rows("q", q, D)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    _want(out.shape == q.shape and out.dtype == torch.bfloat16 and out.is_contiguous(), "out must be contiguous bf16 of q's shape")
+    _want(lse is None or (lse.shape == (T, Hq) and lse.dtype == torch.float32 and lse.is_contiguous()),
+          "lse must be contiguous fp32 [tokens, q_heads]")
+    batch = _batch(cu_seqlens, kv_lens, block_table, max_q)
+    if workspace is None:
+        n = int(lib.wlq_kv4_attention_workspace(T, batch[2], batch[3], max_kv, Hq, H, D))
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.wlq_kv4_attention(qp, qs, T, Hq, H, D, batch[0], batch[1], batch[2], batch[3], max_kv, batch[4], batch[5], *ptrs,
+                                 D ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), _ptr(lse),
+                                 _ptr(workspace), ws_n, _stream(stream)))
+    return out
 
 
 def get_status(stream=None) -> int:

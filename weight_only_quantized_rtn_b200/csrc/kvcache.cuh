@@ -1,0 +1,425 @@
+// kvcache.cuh -- the steps between an attention layer's projections and its
+// attention ("Joy-face_change_optimized" model card: fused ops row, QK-norm +
+// 3D RoPE; section 1, the KV-dtype setting, cached keys and values quantized
+// with scales per token and head):
+//
+//   qk_norm_rope_kernel  norms of queries and keys for each head, rotated by
+//                        their positions (up to four axes), one pass
+//   kv4_append_kernel    the same for keys, then keys and values rounded to
+//                        4 bits and written into a paged cache
+//   kv4_read_kernel      cached rows back as bf16
+//
+// Norm and rotation of one row x (a head's D values of one token):
+//   r = 1 / sqrt(mean x^2 + eps),  n_d = x_d w_d r,
+//   a pair (a, b) of rotated inputs becomes (a c - b s, a s + b c) with
+//   c, s = cos, sin of position(axis of the pair) * inv_freq(pair).
+// The result is rounded ONCE to bf16, and to the bf16 value nearest to the
+// real number: a key that lands on the other side of a border would change a
+// 4-bit code by a whole step, so the fused append has to round as any other
+// exact evaluation does.  The fp32 evaluation is within
+//   E = 2^-20 r (|a| + |b|)
+// of the real value: c and s within 2^-22 (the angle is reduced in fp64 and
+// rounded to fp32 turns, 2 pi 2^-26, then sincospif's two units), r within
+// 8 * 2^-24 (at most 11 additions of one-signed terms, halved by the root,
+// and the roundings of mean, sum and root), x w exact (8 + 8 bits), and three
+// more roundings.  Where a bf16 midpoint lies within E (about one value in a
+// thousand) that value is evaluated again in fp64 and rounded from there.
+//
+// Bound: HBM.  A row is read and written once; 16 (D = 128) or 8 (D = 64)
+// lanes hold it, 8 adjacent values each (one 16-byte load), so the norm is a
+// shuffle reduction and the half-split partner one shuffle.  The angles of a
+// token are reduced once per CTA, which then walks the token's heads with
+// cos and sin in registers.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include "ptx.cuh"
+#include "kvslot.h"
+#include "quantize_ext.cuh"
+
+namespace wlq {
+
+constexpr int ROPE_MAX_AXES = 4;
+constexpr int ROPE_MAX_PAIRS = 64;
+constexpr int KV_THREADS = 256;
+// 4-bit cache rows hold values up to this magnitude: with a scale of
+// fp16(a / 7) every code times its scale stays finite in fp16.
+constexpr float KV4_MAX_ABS = 65280.0f;  // the largest bf16 below 2^16
+
+struct RopeArgs {
+    const int32_t* pos;     // [tokens, axes] or null: no rotation
+    const float* inv_freq;  // [rot / 2]
+    int axes;
+    int pairs;                   // rot / 2
+    int sec_end[ROPE_MAX_AXES];  // pairs [sec_end[a - 1], sec_end[a]) turn by axis a
+    double eps;
+};
+
+// One projection's rows: token t, head h at x + t * stride + h * D.
+struct HeadRows {
+    const uint16_t* x;
+    int64_t stride;
+    int heads;
+    const uint16_t* w;  // [D] norm weight, or null: no norm
+    uint16_t* out;      // token t, head h at out + t * out_stride + h * D
+    int64_t out_stride;
+};
+
+// A paged 4-bit cache: codes [page][head][token][D / 2], scales
+// [page][head][token][D / group] fp16.  A word holds 8 codes + 8: input t of
+// the word at nibble t / 2 (even t) or 4 + t / 2 (odd t), as in the packed
+// int4 weights.
+struct Kv4Pool {
+    uint8_t* k;
+    __half* ks;
+    uint8_t* v;
+    __half* vs;
+    int64_t pages;
+    int page_shift;  // log2 of the tokens of a page
+    int heads;
+    int lg_group;
+};
+
+// Sequences of a call: sequence b has tokens cu[b] .. cu[b + 1] of this call,
+// the last ones of its kv_len[b] cached tokens, on pages table[b][...].
+struct KvBatch {
+    const int32_t* cu;
+    const int32_t* kv_len;
+    const int32_t* table;
+    int64_t table_stride;
+    int batch;
+    int max_q;
+    int64_t tokens;  // rows of the token-indexed tensors
+};
+
+__device__ __forceinline__ void unpack8(uint4 u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint32_t bf16_rn_bits(float y) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(y));
+}
+
+// The bf16 value nearest to a double: the fp32 value nearest to it rounds the
+// same way unless it lies on a bf16 midpoint that the double does not; it is
+// then moved one unit towards the double.
+__device__ __noinline__ uint32_t bf16_from_f64(double y) {
+    float f = static_cast<float>(y);
+    if ((__float_as_uint(f) & 0xFFFFu) == 0x8000u) {
+        const double d = fabs(y) - fabs(static_cast<double>(f));
+        if (d > 0.0) f = __uint_as_float(__float_as_uint(f) + 1u);
+        else if (d < 0.0) f = __uint_as_float(__float_as_uint(f) - 1u);
+    }
+    return bf16_rn_bits(f);
+}
+
+// The token's turns (angle / 2 pi, reduced to [-1/2, 1/2]) for each pair.
+__device__ __forceinline__ void token_turns(const RopeArgs& a, int64_t token, double* turns) {
+    for (int i = threadIdx.x; i < a.pairs; i += blockDim.x) {
+        int ax = 0;
+#pragma unroll
+        for (int k = 0; k < ROPE_MAX_AXES - 1; ++k)
+            if (k + 1 < a.axes && i >= a.sec_end[k]) ax = k + 1;
+        // the angle has at most 31 + 24 bits; 1 / (2 pi) as a sum of two doubles keeps its turns to
+        // about 2^-53 at any position
+        const double angle = static_cast<double>(a.pos[token * a.axes + ax]) * static_cast<double>(a.inv_freq[i]);
+        const double t = angle * 0.15915494309189535;
+        const double rest = fma(angle, -9.839338337591243e-18, fma(angle, 0.15915494309189535, -t));
+        turns[i] = (t - rint(t)) + rest;
+    }
+}
+
+// Lane l (of the row's D / 8) holds inputs 8 l .. 8 l + 7.
+template <int D, bool INTER>
+struct RopeLane {
+    float c[INTER ? 4 : 8], s[INTER ? 4 : 8];
+    int src;  // half-split: the lane with the partners
+    __device__ __forceinline__ void load(const RopeArgs& a, const double* turns, int lane) {
+        constexpr int LPR = D / 8;
+        const int l = lane & (LPR - 1), base = lane & ~(LPR - 1);
+        if constexpr (INTER) {
+            src = lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                c[i] = 1.0f;
+                s[i] = 0.0f;
+                if (4 * l + i < a.pairs) sincospif(static_cast<float>(2.0 * turns[4 * l + i]), &s[i], &c[i]);
+            }
+        } else {
+            const int h8 = a.pairs >> 3;
+            const bool lo = l < h8, rot = l < 2 * h8;
+            src = base + (lo ? l + h8 : (rot ? l - h8 : l));
+            const int p0 = 8 * (lo ? l : l - h8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                c[i] = 1.0f;
+                s[i] = 0.0f;
+                if (rot) {
+                    sincospif(static_cast<float>(2.0 * turns[p0 + i]), &s[i], &c[i]);
+                    if (lo) s[i] = -s[i];  // the first of the pair: a c - b s
+                }
+            }
+        }
+    }
+};
+
+// One row: x (8 bf16 values a lane) to the rounded bits, two per word.
+template <int D, bool INTER>
+__device__ __forceinline__ uint4 norm_rope_row(uint4 raw, const float (&w)[8], bool norm, bool rope, const RopeArgs& a,
+                                               const RopeLane<D, INTER>& R, const double* turns, int lane) {
+    constexpr int LPR = D / 8;
+    if (!norm && !rope) return raw;
+    float x[8];
+    unpack8(raw, x);
+    float r = 1.0f;
+    if (norm) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        r = __frsqrt_rn(fmaf(ss, 1.0f / D, static_cast<float>(a.eps)));
+    }
+    float xw[8], p[8], y[8];
+    uint32_t near = 0;  // values whose rounding the fp32 evaluation does not decide
+#pragma unroll
+    for (int i = 0; i < 8; ++i) xw[i] = x[i] * w[i];  // exact: 8 x 8 bits
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float c = 1.0f, s = 0.0f;
+        if constexpr (INTER) {
+            p[i] = xw[i ^ 1];
+            c = R.c[i / 2];
+            s = (i & 1) ? R.s[i / 2] : -R.s[i / 2];
+        } else {
+            p[i] = __shfl_sync(0xffffffffu, xw[i], R.src);
+            c = R.c[i];
+            s = R.s[i];
+        }
+        y[i] = fmaf(xw[i], c, p[i] * s) * r;
+        const float mid = __uint_as_float((__float_as_uint(y[i]) & 0xFFFF0000u) | 0x8000u);
+        const float e = (fabsf(xw[i]) + fabsf(p[i])) * (r * 9.5367431640625e-7f);  // E above
+        if (fabsf(y[i] - mid) <= e) near |= 1u << i;
+    }
+    uint4 out;
+    uint32_t* o = reinterpret_cast<uint32_t*>(&out);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+        o[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    if (__any_sync(0xffffffffu, near != 0)) {
+        double r64 = 1.0;
+        if (norm) {
+            double ss = 0.0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), ss);
+#pragma unroll
+            for (int k = LPR / 2; k > 0; k >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
+            r64 = 1.0 / sqrt(ss / D + a.eps);
+        }
+        const int l = lane & (LPR - 1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (!(near >> i & 1u)) continue;
+            double c = 1.0, s = 0.0;
+            int pair = -1;
+            bool first = false;
+            if constexpr (INTER) {
+                if (4 * l + i / 2 < a.pairs) pair = 4 * l + i / 2;
+                first = (i & 1) == 0;
+            } else {
+                const int h8 = a.pairs >> 3;
+                first = l < h8;
+                if (l < 2 * h8) pair = 8 * (first ? l : l - h8) + i;
+            }
+            if (rope && pair >= 0) sincospi(2.0 * turns[pair], &s, &c);
+            if (first) s = -s;
+            const uint32_t b = bf16_from_f64((static_cast<double>(xw[i]) * c + static_cast<double>(p[i]) * s) * r64);
+            o[i / 2] = (i & 1) ? ((o[i / 2] & 0xFFFFu) | (b << 16)) : ((o[i / 2] & 0xFFFF0000u) | b);
+        }
+    }
+    return out;
+}
+
+__device__ __forceinline__ void load_weight8(const uint16_t* w, int l, float (&f)[8]) {
+    if (w) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(static_cast<uint32_t>(w[8 * l + i]) << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = 1.0f;
+    }
+}
+
+// grid (tokens, splits of the token's rows); a CTA takes rows y, y + splits, ...
+// in warp-sized bites of 32 / LPR rows.
+template <int D, bool INTER>
+__global__ void __launch_bounds__(KV_THREADS) qk_norm_rope_kernel(const HeadRows q, const HeadRows k, const RopeArgs a,
+                                                                  int64_t tokens) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    __shared__ double turns[ROPE_MAX_PAIRS];
+    grid_dependency_sync();
+    const int64_t token = blockIdx.x;
+    const bool rope = a.pos != nullptr;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (LPR - 1), sub = lane / LPR;
+    if (rope) token_turns(a, token, turns);
+    __syncthreads();
+    RopeLane<D, INTER> R;
+    R.load(a, turns, lane);
+    const int step = gridDim.y * (KV_THREADS / 32);
+    const int bites_q = (q.heads + RPW - 1) / RPW, bites = bites_q + (k.heads + RPW - 1) / RPW;
+    float w[8];
+    int held = -1;  // whose weight w holds
+    for (int b = blockIdx.y * (KV_THREADS / 32) + warp; b < bites; b += step) {
+        const bool isq = b < bites_q;
+        const HeadRows& S = isq ? q : k;
+        if (held != static_cast<int>(isq)) {
+            load_weight8(S.w, l, w);
+            held = static_cast<int>(isq);
+        }
+        const int h = (isq ? b : b - bites_q) * RPW + sub;
+        const bool in = h < S.heads;
+        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+        if (in) raw = *reinterpret_cast<const uint4*>(S.x + token * S.stride + static_cast<int64_t>(h) * D + 8 * l);
+        const uint4 o = norm_rope_row<D, INTER>(raw, w, S.w != nullptr, rope, a, R, turns, lane);
+        if (in) *reinterpret_cast<uint4*>(S.out + token * S.out_stride + static_cast<int64_t>(h) * D + 8 * l) = o;
+    }
+}
+
+// The cached position of token i of sequence b: its page and place, or -1
+// (an offset or page out of range: recorded, nothing is read or written).
+struct KvSlot {
+    int64_t page;
+    int place;
+    int64_t row;  // in the token-indexed tensors
+};
+__device__ __forceinline__ bool kv_slot(const KvBatch& B, const Kv4Pool& P, int b, int i, KvSlot& s) {
+    const int64_t r0 = B.cu[b], r1 = B.cu[b + 1], kv_len = B.kv_len[b];
+    const KvRange seq = kv_sequence(r0, r1, kv_len, B.max_q, B.tokens);
+    if (seq == KV_OK && i >= r1 - r0) return false;
+    int64_t entry;
+    bool ok = seq == KV_OK && kv_entry(kv_len - (r1 - r0) + i, B.table_stride, P.page_shift, &entry, &s.place) == KV_OK;
+    if (ok) {
+        s.page = B.table[b * B.table_stride + entry];
+        s.row = r0 + i;
+        ok = kv_page_ok(s.page, P.pages);
+    }
+    if (!ok && seq != KV_NONE) raise_error(ERRBIT_INDEX);
+    return ok;
+}
+
+// Element index of (slot, head) in units of rows of D codes.
+__device__ __forceinline__ int64_t kv_row(const Kv4Pool& P, const KvSlot& s, int h) {
+    return ((s.page * P.heads + h) << P.page_shift) + s.place;
+}
+
+// 8 codes (bytes, two's complement, two words) as one word of the cache.
+__device__ __forceinline__ uint32_t kv4_word(uint32_t c0, uint32_t c1) {
+    c0 = __vadd4(c0, 0x08080808u);
+    c1 = __vadd4(c1, 0x08080808u);
+    return __byte_perm(c0 | (c0 >> 12), c1 | (c1 >> 12), 0x5140);
+}
+
+// grid (max_q * batch, splits of the token's 2 H rows): key rows, then value
+// rows, a warp-sized bite at a time.
+template <int D, bool INTER>
+__global__ void __launch_bounds__(KV_THREADS) kv4_append_kernel(const HeadRows k, const HeadRows v, const RopeArgs a,
+                                                                const KvBatch B, const Kv4Pool P) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    __shared__ double turns[ROPE_MAX_PAIRS];
+    grid_dependency_sync();
+    const int b = blockIdx.x / B.max_q, i = blockIdx.x - b * B.max_q;
+    KvSlot slot;
+    if (!kv_slot(B, P, b, i, slot)) return;  // the same for the whole CTA
+    const bool rope = a.pos != nullptr;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (LPR - 1), sub = lane / LPR;
+    if (rope) token_turns(a, slot.row, turns);
+    __syncthreads();
+    RopeLane<D, INTER> R;
+    R.load(a, turns, lane);
+    float w[8];
+    load_weight8(k.w, l, w);
+    const int step = gridDim.y * (KV_THREADS / 32);
+    const int bites_k = (P.heads + RPW - 1) / RPW;
+    const int lg8 = P.lg_group - 3;  // log2 of the lanes of a group
+    bool bad = false;
+    for (int t = blockIdx.y * (KV_THREADS / 32) + warp; t < 2 * bites_k; t += step) {
+        const bool isk = t < bites_k;
+        const int h = (isk ? t : t - bites_k) * RPW + sub;
+        const bool in = h < P.heads;
+        const HeadRows& S = isk ? k : v;
+        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+        if (in) raw = *reinterpret_cast<const uint4*>(S.x + slot.row * S.stride + static_cast<int64_t>(h) * D + 8 * l);
+        if (isk) raw = norm_rope_row<D, INTER>(raw, w, k.w != nullptr, rope, a, R, turns, lane);
+        uint32_t m2 = __vmaxu2(__vmaxu2(raw.x & 0x7FFF7FFFu, raw.y & 0x7FFF7FFFu),
+                               __vmaxu2(raw.z & 0x7FFF7FFFu, raw.w & 0x7FFF7FFFu));
+        uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+        for (int o = (1 << lg8) >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float amax = __uint_as_float(m << 16);
+        const bool gbad = !(amax <= KV4_MAX_ABS);  // too large, an infinity or a NaN
+        const float s = gbad ? 0.0f : stored_scale<SCALE_F16>(amax, 7);
+        bad |= gbad && in;
+        uint32_t c0 = 0, c1 = 0;
+        if (s > 0.0f) {
+            float f[8];
+            unpack8(raw, f);
+            const float inv = __frcp_rn(s);
+            c0 = rtn4_f32_clamped(make_float4(f[0], f[1], f[2], f[3]), s, inv, 0.5f * s, 7.0f);
+            c1 = rtn4_f32_clamped(make_float4(f[4], f[5], f[6], f[7]), s, inv, 0.5f * s, 7.0f);
+        }
+        if (in) {
+            const int64_t row = kv_row(P, slot, h);
+            reinterpret_cast<uint32_t*>(isk ? P.k : P.v)[row * LPR + l] = kv4_word(c0, c1);
+            if ((l & ((1 << lg8) - 1)) == 0)
+                (isk ? P.ks : P.vs)[row * (LPR >> lg8) + (l >> lg8)] = __float2half_rn(s);
+        }
+    }
+    if (bad) raise_error(ERRBIT_NONFINITE);
+}
+
+// Two bf16 values code * scale (one rounding) of nibble pairs of a word.
+__device__ __forceinline__ uint4 kv4_values(uint32_t word, float s) {
+    uint4 out;
+    uint32_t* o = reinterpret_cast<uint32_t*>(&out);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // inputs 2 j (nibble j) and 2 j + 1 (nibble 4 + j)
+        const float lo = static_cast<float>(static_cast<int>(word >> (4 * j) & 15u) - 8) * s;
+        const float hi = static_cast<float>(static_cast<int>(word >> (16 + 4 * j) & 15u) - 8) * s;
+        const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+        o[j] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    return out;
+}
+
+template <int D>
+__global__ void __launch_bounds__(KV_THREADS) kv4_read_kernel(uint16_t* __restrict__ k_out, uint16_t* __restrict__ v_out,
+                                                              const KvBatch B, const Kv4Pool P) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    grid_dependency_sync();
+    const int b = blockIdx.x / B.max_q, i = blockIdx.x - b * B.max_q;
+    KvSlot slot;
+    if (!kv_slot(B, P, b, i, slot)) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (LPR - 1), sub = lane / LPR;
+    const int step = gridDim.y * (KV_THREADS / 32);
+    const int bites_k = (P.heads + RPW - 1) / RPW;
+    const int lg8 = P.lg_group - 3;
+    for (int t = blockIdx.y * (KV_THREADS / 32) + warp; t < 2 * bites_k; t += step) {
+        const bool isk = t < bites_k;
+        const int h = (isk ? t : t - bites_k) * RPW + sub;
+        if (h >= P.heads) continue;
+        const int64_t row = kv_row(P, slot, h);
+        const uint32_t word = reinterpret_cast<const uint32_t*>(isk ? P.k : P.v)[row * LPR + l];
+        const float s = __half2float((isk ? P.ks : P.vs)[row * (LPR >> lg8) + (l >> lg8)]);
+        uint16_t* out = (isk ? k_out : v_out) + (slot.row * P.heads + h) * D + 8 * l;
+        *reinterpret_cast<uint4*>(out) = kv4_values(word, s);
+    }
+}
+
+}  // namespace wlq

@@ -10,7 +10,7 @@
 namespace wlq {
 
 // Device error word (one per device that loads the library).
-enum : unsigned { ERRBIT_NONFINITE = 1u, ERRBIT_TIMEOUT = 2u, ERRBIT_LAUNCH = 4u };
+enum : unsigned { ERRBIT_NONFINITE = 1u, ERRBIT_TIMEOUT = 2u, ERRBIT_LAUNCH = 4u, ERRBIT_INDEX = 8u };
 __device__ unsigned int g_error_word;
 
 __device__ __forceinline__ void raise_error(unsigned bit) { atomicOr(&g_error_word, bit); }

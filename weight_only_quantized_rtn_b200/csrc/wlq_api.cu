@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -24,6 +25,8 @@
 #include "ptx.cuh"
 #include "quantize.cuh"
 #include "nvfp4.cuh"
+#include "kvcache.cuh"
+#include "kv4_decode.cuh"
 
 namespace {
 
@@ -1407,6 +1410,7 @@ wlq_status wlq_get_status(void* stream) {
     }
     if (word & wlq::ERRBIT_TIMEOUT) return fail(WLQ_ERR_TIMEOUT, "a bounded device wait ran out");
     if (word & wlq::ERRBIT_NONFINITE) return fail(WLQ_ERR_NONFINITE, "non-finite weight");
+    if (word & wlq::ERRBIT_INDEX) return fail(WLQ_ERR_INDEX, "an offset, length or page out of range");
     if (word & wlq::ERRBIT_LAUNCH) return fail(WLQ_ERR_CUDA, "a kernel was launched with a shape it cannot run");
     return WLQ_OK;
 }
@@ -1672,3 +1676,5 @@ wlq_status wlq_w4a4_linear(const void* x, int64_t M, const void* wq, const void*
 }
 
 }  // extern "C"
+
+#include "attn_api.cuh"
