@@ -476,6 +476,33 @@ wlq_status wlq_kv4_attention(const void* q, int64_t q_stride, int64_t tokens, in
                              float scale, int causal, int window, void* out, float* lse, void* workspace,
                              size_t ws_bytes, void* stream);
 
+/*
+ * The Linear in 8-bit integers with a scale for each token and each output
+ * channel (the W8A8 form of the card's int8 Linear):
+ *   y[m, n] = xs[m] ws[n] sum_k xq[m, k] wq[n, k] + b[n]
+ * The sum is exact (32-bit integers on the tensor cores); the scales and the
+ * bias are applied in fp32, then one rounding to y_dtype.
+ * xq, xs: int8 [M, K] codes and fp32 [M] scales (wlq_quantize_ex, bits 8,
+ *         group 0, fp32 scales)
+ * wq, ws: int8 [N, K] codes and fp32 [N] scales (wlq_quantize, bits 8, group 0)
+ * bias  : bf16 [N] or NULL; y: [M, N] in y_dtype
+ * K % 16 == 0, K <= 131056 (the sum fits 32 bits for any int8 codes); xq and
+ * wq 16-byte aligned.  M == 0 or N == 0 is a no-op.
+ */
+wlq_status wlq_int8_linear(const void* xq, const float* xs, int64_t M, const void* wq, const float* ws, int64_t N,
+                           int64_t K, const void* bias, void* y, int y_dtype, void* stream);
+
+/*
+ * The same from bf16 x [M, K], which is quantized token by token in the
+ * workspace (xs = fp32(max|x| / 127), codes as wlq_quantize_ex, bit-identical)
+ * and then goes through wlq_int8_linear.  A non-finite x sets
+ * WLQ_ERR_NONFINITE; that token's codes and scale are 0.  workspace:
+ * wlq_w8a8_workspace() bytes, 16-byte aligned.
+ */
+size_t wlq_w8a8_workspace(int64_t M, int64_t K);
+wlq_status wlq_w8a8_linear(const void* x, int64_t M, const void* wq, const float* ws, int64_t N, int64_t K,
+                           const void* bias, void* y, int y_dtype, void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -43,7 +43,7 @@ def norm_rope(x, weight, eps, positions, inv_freq, sections, interleaved):
 
 def quantize4(x, group):
     """fp64 values of bf16 x [..., D] -> (codes, fp16 scales as fp64 [..., D / group])."""
-    g = x.reshape(*x.shape[:-1], -1, group)
+    g = x.reshape(*x.shape[:-1], x.shape[-1] // group, group)
     s = (np.abs(g).max(-1) / 7).astype(np.float16).astype(np.float64)
     with np.errstate(divide="ignore", invalid="ignore"):
         q = np.where(s[..., None] > 0, np.clip(np.rint(g / s[..., None]), -7, 7), 0.0)
@@ -62,59 +62,65 @@ def pack4(q):
 
 
 def unpack4(b, D):
-    words = np.ascontiguousarray(b).view(np.uint32).reshape(*b.shape[:-1], D // 8)
-    q = np.zeros((*b.shape[:-1], D), dtype=np.int8)
-    for d in range(D):
-        t = d % 8
-        nib = t // 2 if t % 2 == 0 else 4 + t // 2
-        q[..., d] = ((words[..., d // 8] >> np.uint32(4 * nib)) & 15).astype(np.int8) - 8
-    return q
+    words = np.ascontiguousarray(b).view(np.uint32).reshape(*b.shape[:-1], D // 8, 1)
+    t = np.arange(8)
+    nib = np.where(t % 2 == 0, t // 2, 4 + t // 2)
+    return (((words >> (4 * nib).astype(np.uint32)) & 15).astype(np.int8) - 8).reshape(*b.shape[:-1], D)
 
 
-def cache_values(cache, which, pages, head, n):
-    """The first n tokens' values [n, D] (fp64) of one head on the given pages (-1 pages give NaN rows)."""
-    codes, scales = (cache[0], cache[1]) if which == "k" else (cache[2], cache[3])
-    P, D, G = codes.shape[2], codes.shape[3] * 2, scales.shape[3]
-    out = np.full((len(pages) * P, D), np.nan)
-    for i, p in enumerate(pages):
-        if 0 <= p < codes.shape[0]:
-            q = unpack4(codes[p, head].cpu().numpy(), D).astype(np.float64)
-            s = f64(scales[p, head])
-            out[i * P:(i + 1) * P] = (q.reshape(P, G, -1) * s[..., None]).reshape(P, D)
-    return out[:n]
+def cache_values(codes, scales, pages, n):
+    """The first n cached tokens' values [heads, n, D] (fp64, the tensors' device) on the given pages; NaN on pages out of range."""
+    P, half, G = codes.shape[2], codes.shape[3], scales.shape[3]
+    H, D = codes.shape[1], 2 * half
+    pages = torch.as_tensor(np.asarray(pages, dtype=np.int64), device=codes.device)
+    ok = (pages >= 0) & (pages < codes.shape[0])
+    at = torch.where(ok, pages, torch.zeros_like(pages))
+    c, s = codes[at], scales[at].double()
+    shift = torch.tensor([4 * (t // 2 if t % 2 == 0 else 4 + t // 2) for t in range(8)], device=codes.device)
+    w = c.contiguous().view(torch.int32).long() & 0xFFFFFFFF
+    q = ((w[..., None] >> shift) & 15).double() - 8
+    v = (q.reshape(len(pages), H, P, G, D // G) * s[..., None]).reshape(len(pages), H, P, D)
+    v[~ok] = float("nan")
+    return v.transpose(0, 1).reshape(H, -1, D)[:, :n]
 
 
-def attention(q, cache, cu, kv_lens, table, kv_heads, scale, causal, window):
-    """(out [T, Hq, D], lse [T, Hq]) in fp64; rows of no sequence are NaN; a query that sees nothing has 0, -inf."""
+def attention(q, cache, cu, kv_lens, table, scale, causal, window):
+    """The 64-bit attention and what its error bounds need: a dict of fp64 arrays
+    out, lse, E (the largest score error of fp16 keys), A (sum_j p_j |v_j|), B
+    (2^-25 sum_j |v_j|).  Rows of no sequence are NaN; a query that sees
+    nothing has out 0 and lse -inf."""
     T, Hq, D = q.shape
-    out, lse = np.full((T, Hq, D), np.nan), np.full((T, Hq), np.nan)
-    share = Hq // kv_heads
-    P = cache[0].shape[2]
+    dev = cache[0].device
+    r = {k: torch.full((T, Hq) + ((D,) if k in ("out", "A", "B") else ()), float("nan"), dtype=torch.float64, device=dev)
+         for k in ("out", "lse", "E", "A", "B")}
+    q = q.double()
+    P, hk = cache[0].shape[2], cache[0].shape[1]
+    share = Hq // hk
     for b in range(len(kv_lens)):
-        n, kv = cu[b + 1] - cu[b], kv_lens[b]
-        pages = table[b][: -(-kv // P)]
-        i, j = np.arange(n)[:, None] + (kv - n), np.arange(kv)[None]
-        seen = np.ones((n, kv), dtype=bool)
+        n, kv = int(cu[b + 1] - cu[b]), int(kv_lens[b])
+        if n == 0:
+            continue
+        rows, pages = slice(int(cu[b]), int(cu[b + 1])), table[b][: -(-kv // P)]
+        k, v = cache_values(cache[0], cache[1], pages, kv), cache_values(cache[2], cache[3], pages, kv)
+        there = ~torch.isnan(k[0, :, 0])
+        k, v = torch.where(there[:, None], k, 0.0), torch.where(there[:, None], v, 0.0)
+        i, j = torch.arange(n, device=dev)[:, None] + (kv - n), torch.arange(kv, device=dev)
+        seen = torch.ones(n, kv, dtype=torch.bool, device=dev)
         if causal:
             seen = j <= i
             if window:
                 seen = seen & (j > i - window)
-        for h in range(kv_heads):
-            if kv:
-                k, v = cache_values(cache, "k", pages, h, kv), cache_values(cache, "v", pages, h, kv)
-                there = ~np.isnan(k[:, 0])
-                k, v = np.nan_to_num(k), np.nan_to_num(v)
-            else:
-                k = v = np.zeros((0, D))
-                there = np.zeros(0, dtype=bool)
-            for g in range(share):
-                z = q[cu[b]:cu[b + 1], h * share + g] @ k.T * scale
-                z = np.where(seen & there, z, -np.inf)
-                top = z.max(-1, initial=-np.inf, keepdims=True)
-                e = np.exp(z - np.where(np.isfinite(top), top, 0.0))
-                l = e.sum(-1)
-                rows = slice(cu[b], cu[b + 1])
-                out[rows, h * share + g] = (e @ v) / np.where(l > 0, l, 1.0)[:, None]
-                with np.errstate(divide="ignore"):
-                    lse[rows, h * share + g] = np.where(l > 0, np.log(l), -np.inf) + np.where(np.isfinite(top[:, 0]), top[:, 0], 0.0)
-    return out, lse
+        seen = seen & there
+        for h in range(Hq):
+            kh, vh = k[h // share], v[h // share]
+            z = torch.where(seen, q[rows, h] @ kh.T * scale, float("-inf"))
+            top = z.amax(-1, keepdim=True)
+            top = torch.where(torch.isinf(top), 0.0, top)
+            e = torch.exp(z - top)
+            l = e.sum(-1, keepdim=True)
+            p = e / torch.where(l > 0, l, 1.0)
+            r["out"][rows, h], r["A"][rows, h] = p @ vh, p @ vh.abs()
+            r["lse"][rows, h] = (torch.log(l) + top)[:, 0]
+            r["E"][rows, h] = (q[rows, h].abs() @ kh.abs().T).amax(-1) * abs(scale) * (2.0 ** -11 + 2.0 ** -20)
+            r["B"][rows, h] = vh.abs().sum(0) * 2.0 ** -25
+    return {k: x.cpu().numpy() for k, x in r.items()}

@@ -111,3 +111,42 @@ def test_attention_workspace():
     assert f(0, 1, 1, 100, 8, 8, 128) == 0 and f(1, 1, 1, 100, 8, 3, 128) == 0 and f(1, 1, 1, 100, 8, 8, 96) == 0
     assert f(1, 1, 1, 64, 8, 8, 128) == 0                      # too short to split
     assert f(1, 1, 1, 1 << 20, 8, 8, 128) >= 8 * 2 * (128 + 2) * 4  # at least two parts a row
+
+
+def int8(**kw):
+    a = dict(xq=P, xs=P, M=4, wq=P, ws=P, N=64, K=128, bias=None, y=P, y_dtype=0, stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return m.lib.wlq_int8_linear(*a.values())
+
+
+def w8a8(**kw):
+    a = dict(xq=P, M=4, wq=P, ws=P, N=64, K=128, bias=None, y=P, y_dtype=0, workspace=P, ws_bytes=1 << 40, stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return m.lib.wlq_w8a8_linear(*a.values())
+
+
+BAD_INT8 = [
+    (m.ERR_INVALID_ARG, dict(M=-1)), (m.ERR_INVALID_ARG, dict(N=-1)), (m.ERR_SHAPE, dict(K=0)), (m.ERR_SHAPE, dict(K=24)),
+    (m.ERR_SHAPE, dict(K=131072)), (m.ERR_INVALID_ARG, dict(y_dtype=2)), (m.ERR_INVALID_ARG, dict(xq=None)), (m.ERR_INVALID_ARG, dict(wq=None)),
+    (m.ERR_INVALID_ARG, dict(ws=None)), (m.ERR_INVALID_ARG, dict(y=None)), (m.ERR_ALIGN, dict(xq=P + 8)), (m.ERR_ALIGN, dict(wq=P + 4)),
+    (m.ERR_ALIGN, dict(ws=P + 2)), (m.ERR_ALIGN, dict(y=P + 2)), (m.ERR_ALIGN, dict(bias=P + 1)), (m.ERR_SHAPE, dict(M=1 << 31)),
+    (m.ERR_SHAPE, dict(M=1 << 30, N=1 << 30)),
+]
+
+
+@pytest.mark.parametrize("want,kw", BAD_INT8 + [(m.ERR_INVALID_ARG, dict(xs=None)), (m.ERR_ALIGN, dict(xs=P + 2))])
+def test_int8_refuses(want, kw):
+    assert int8(**kw) == want
+
+
+@pytest.mark.parametrize("want,kw", BAD_INT8 + [(m.ERR_WORKSPACE, dict(workspace=None)), (m.ERR_WORKSPACE, dict(ws_bytes=100)),
+                                                (m.ERR_ALIGN, dict(workspace=P + 8))])
+def test_w8a8_refuses(want, kw):
+    assert w8a8(**kw) == want
+
+
+def test_int8_of_nothing_is_a_no_op():
+    assert int8(M=0) == m.OK and int8(N=0) == m.OK and w8a8(M=0) == m.OK and w8a8(N=0) == m.OK
+    assert m.w8a8_workspace(4, 128) >= 4 * 128 + 16 and m.w8a8_workspace(0, 128) == 0 and m.w8a8_workspace(4, 24) == 0

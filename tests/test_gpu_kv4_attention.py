@@ -46,32 +46,16 @@ def make(seed, q_lens, kv_lens, hk, share, D, group, page, extra_pages=3, pool=N
         for t in (cache[0], cache[2]):
             t.copy_(torch.randint(0, 256, t.shape, generator=g, dtype=torch.uint8))
     for b, kv in enumerate(kv_lens):
-        for p in range(-(-kv // page)):
-            n, pg = min(page, kv - p * page), int(table[b, p])
-            for ci, spread in ((0, 2.0), (2, 1.0)):
-                x = torch.randn(hk, n, D, generator=g) * torch.exp(0.5 * spread * torch.randn(hk, n, 1, generator=g))
-                q, s = ref.quantize4(ref.f64(x.bfloat16()), group)
-                cache[ci][pg, :, :n] = torch.from_numpy(ref.pack4(q)).cuda()
-                cache[ci + 1][pg, :, :n] = torch.from_numpy(s.astype(np.float16)).cuda()
+        j = torch.arange(kv)
+        pg, place = table[b, j // page].long().cuda(), (j % page).cuda()
+        for ci, spread in ((0, 2.0), (2, 1.0)):
+            x = torch.randn(kv, hk, D, generator=g) * torch.exp(0.5 * spread * torch.randn(kv, hk, 1, generator=g))
+            c, s = ref.quantize4(ref.f64(x.bfloat16()), group)
+            cache[ci][pg, :, place] = torch.from_numpy(ref.pack4(c)).cuda()
+            cache[ci + 1][pg, :, place] = torch.from_numpy(s.astype(np.float16)).cuda()
     q = torch.randn(T, hk * share, D, generator=g).bfloat16()
     q[int(cu[-1]):] = float("nan")
     return q.cuda(), cache, cu, np.array(kv_lens, dtype=np.int32), table.numpy()
-
-
-def bounds(q, cache, cu, kv_lens, table, hk, scale):
-    """E [T, Hq] and B [T, Hq, D]: see the module's text."""
-    T, Hq, D = q.shape
-    E, B = np.zeros((T, Hq)), np.zeros((T, Hq, D))
-    P = cache[0].shape[2]
-    for b in range(len(kv_lens)):
-        pages = table[b][: -(-kv_lens[b] // P)]
-        for h in range(Hq):
-            if kv_lens[b]:
-                k = np.nan_to_num(np.abs(ref.cache_values(cache, "k", pages, h // (Hq // hk), kv_lens[b])))
-                E[cu[b]:cu[b + 1], h] = (np.abs(q[cu[b]:cu[b + 1], h]) @ k.T).max(-1) * abs(scale) * (2.0 ** -11 + 2.0 ** -20)
-                v = np.nan_to_num(np.abs(ref.cache_values(cache, "v", pages, h // (Hq // hk), kv_lens[b])))
-                B[cu[b]:cu[b + 1], h] = v.sum(0) * 2.0 ** -25
-    return E, B
 
 
 def check(m, q, cache, cu, kv, table, hk, causal, window, scale=None, max_q=None, max_kv=None, ws=None, random=True):
@@ -84,10 +68,8 @@ def check(m, q, cache, cu, kv, table, hk, causal, window, scale=None, max_q=None
     m.kv4_attention(q, cache, *dev, max_q, max_kv, scale=scale, causal=causal, window=window, out=out, lse=lse, workspace=ws)
     sc = D ** -0.5 if scale is None else scale
     n = int(cu[-1])
-    qn = ref.f64(q)[:n]
-    want, want_lse = ref.attention(qn, cache, cu, kv, table, hk, sc, causal, window)
-    E, B = bounds(qn, cache, cu, kv, table, hk, sc)
-    A = ref_abs(qn, cache, cu, kv, table, hk, sc, causal, window)
+    r = ref.attention(q, cache, cu, kv, table, sc, causal, window)
+    want, want_lse, E, A, B = (r[k][:n] for k in ("out", "lse", "E", "A", "B"))
     got, got_lse = ref.f64(out), ref.f64(lse)
     assert (got[n:] == -7).all() and (got_lse[n:] == -7).all()  # rows of no sequence
     got, got_lse = got[:n], got_lse[:n]
@@ -101,14 +83,6 @@ def check(m, q, cache, cu, kv, table, hk, causal, window, scale=None, max_q=None
     if random and n * Hq >= 8:
         assert np.linalg.norm(got - want) <= 2.0 ** -8 * np.linalg.norm(want)
     return out, lse
-
-
-def ref_abs(q, cache, cu, kv, table, hk, sc, causal, window):
-    """sum_j p_j |v_j|: the reference with the values' magnitudes (codes mirrored to their absolute value)."""
-    D = q.shape[-1]
-    v = cache[2].cpu().numpy()
-    a = ref.pack4(np.abs(ref.unpack4(v, D)))
-    return ref.attention(q, (cache[0], cache[1], torch.from_numpy(a), cache[3]), cu, kv, table, hk, sc, causal, window)[0]
 
 
 @pytest.mark.parametrize("D,group,page", [(128, 32, 16), (128, 64, 64), (128, 128, 256), (64, 32, 32), (64, 64, 128)])
@@ -132,6 +106,19 @@ def test_chunks(D, page, causal, window, share, q_lens, kv_lens):
     m.check_status()
 
 
+@pytest.mark.parametrize("D,group,page", [(128, 32, 16), (128, 128, 64), (64, 64, 256), (64, 32, 32)])
+@pytest.mark.parametrize("share,q_lens,kv_lens", [
+    (1, [129], [129]), (1, [600, 40], [600, 1500]), (4, [64, 1, 300], [128, 5, 900]), (8, [33, 257], [2000, 257]), (3, [100], [3000])])
+@pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 200)])
+def test_prompts_and_chunks_of_many_rows(D, group, page, share, q_lens, kv_lens, causal, window):
+    m = wlq()
+    a = make(sum(kv_lens) + share, q_lens, kv_lens, 2, share, D, group, page, tail=3)
+    out, _ = check(m, *a, 2, causal, window)
+    again, _ = check(m, *a, 2, causal, window)
+    assert torch.equal(out, again)
+    m.check_status()
+
+
 @pytest.mark.parametrize("kv,window", [(5000, 0), (20011, 0), (20011, 600)])
 def test_long_caches_are_split(kv, window):
     m = wlq()
@@ -150,8 +137,9 @@ def test_scores_that_grow_move_the_maximum():
     """Keys whose scores climb by far more than the lazy maximum's 2^8, then fall; the largest last, first and in between."""
     m = wlq()
     D, n = 64, 257
-    for order in (np.arange(n), np.arange(n)[::-1].copy(), np.abs(np.arange(n) - 128)):
-        q, cache, cu, kv, table = make(11, [3], [n], 1, 2, D, 32, 16)
+    for order, n_q in ((np.arange(n), 3), (np.arange(n)[::-1].copy(), 3), (np.abs(np.arange(n) - 128), 3), (np.arange(n), 90),
+                       (np.arange(n)[::-1].copy(), 90), (np.abs(np.arange(n) - 128), 90)):
+        q, cache, cu, kv, table = make(11, [n_q], [n], 1, 2, D, 32, 16)
         pages = table[0]
         for j in range(n):
             s = np.float16(0.02 * (order[j] + 1))
@@ -198,13 +186,14 @@ def test_a_cache_beyond_four_gigabytes():
 
 def test_pages_out_of_range_count_as_not_seen():
     m = wlq()
-    q, cache, cu, kv, table = make(6, [1, 1], [64, 40], 1, 2, 64, 32, 16)
-    table = table.copy()
-    table[0, 1] = -1
-    table[0, 2] = cache[0].shape[0]
-    table[1, :] = 1 << 30
-    check(m, q, cache, cu, kv, table, 1, True, 0, random=False)
-    assert m.get_status() == m.ERR_INDEX
+    for q_lens in ([1, 1], [30, 40]):
+        q, cache, cu, kv, table = make(6, q_lens, [64, 40], 1, 2, 64, 32, 16)
+        table = table.copy()
+        table[0, 1] = -1
+        table[0, 2] = cache[0].shape[0]
+        table[1, :] = 1 << 30
+        check(m, q, cache, cu, kv, table, 1, True, 0, random=False)
+        assert m.get_status() == m.ERR_INDEX
     # a table narrower than the sequence
     check_table = torch.from_numpy(table[:, :1].copy()).cuda()
     m.kv4_attention(q, cache, torch.from_numpy(cu).cuda(), torch.from_numpy(kv).cuda(), check_table, 1, 64)

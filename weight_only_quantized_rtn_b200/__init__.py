@@ -29,7 +29,8 @@ EXPORTS = ("wlq_quantize", "wlq_quantize_pack", "wlq_quantize_ex", "wlq_quantize
            "wlq_pack", "wlq_unpack", "wlq_linear_workspace", "wlq_linear", "wlq_linear_noalloc",
            "wlq_lowrank_workspace", "wlq_lowrank_split", "wlq_lowrank_residual", "wlq_nvfp4_scales_bytes",
            "wlq_nvfp4_quantize", "wlq_nvfp4_linear_workspace", "wlq_nvfp4_linear", "wlq_w4a4_workspace",
-           "wlq_w4a4_linear", "wlq_qk_norm_rope", "wlq_kv4_append", "wlq_kv4_read", "wlq_kv4_attention", "wlq_get_status",
+           "wlq_w4a4_linear", "wlq_qk_norm_rope", "wlq_kv4_append", "wlq_kv4_read", "wlq_kv4_attention",
+           "wlq_int8_linear", "wlq_w8a8_linear", "wlq_get_status",
            "wlq_probe_wait_timeout", "wlq_set_grid_limit", "wlq_last_error", "wlq_version")
 
 if not os.path.exists(LIB_PATH):
@@ -74,6 +75,10 @@ lib.wlq_kv4_attention_workspace.argtypes = [_i64, _i32, _i32, _i64, _i32, _i32, 
 lib.wlq_kv4_attention_workspace.restype = _sz
 lib.wlq_kv4_attention.argtypes = [_vp, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _i32, _i32, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
                                   _i64, _i32, _i32, ctypes.c_float, _i32, _i32, _vp, _vp, _vp, _sz, _vp]
+lib.wlq_int8_linear.argtypes = [_vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i32, _vp]
+lib.wlq_w8a8_workspace.argtypes = [_i64, _i64]
+lib.wlq_w8a8_workspace.restype = _sz
+lib.wlq_w8a8_linear.argtypes = [_vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i32, _vp, _sz, _vp]
 lib.wlq_get_status.argtypes = [_vp]
 lib.wlq_probe_wait_timeout.argtypes = [_u64, _vp]
 lib.wlq_set_grid_limit.argtypes = [_i32]
@@ -82,7 +87,8 @@ lib.wlq_last_error.restype = ctypes.c_char_p
 lib.wlq_version.restype = ctypes.c_char_p
 for _f in ("wlq_quantize", "wlq_quantize_pack", "wlq_quantize_ex", "wlq_quantize_fp8", "wlq_pack", "wlq_unpack", "wlq_linear",
            "wlq_linear_noalloc", "wlq_lowrank_split", "wlq_lowrank_residual", "wlq_nvfp4_quantize", "wlq_nvfp4_linear",
-           "wlq_w4a4_linear", "wlq_qk_norm_rope", "wlq_kv4_append", "wlq_kv4_read", "wlq_kv4_attention", "wlq_get_status",
+           "wlq_w4a4_linear", "wlq_qk_norm_rope", "wlq_kv4_append", "wlq_kv4_read", "wlq_kv4_attention",
+           "wlq_int8_linear", "wlq_w8a8_linear", "wlq_get_status",
            "wlq_probe_wait_timeout"):
     getattr(lib, _f).restype = ctypes.c_int
 
@@ -497,6 +503,53 @@ def kv4_attention(q, cache, cu_seqlens, kv_lens, block_table, max_q: int, max_kv
                                  D ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), _ptr(lse),
                                  _ptr(workspace), ws_n, _stream(stream)))
     return out
+
+
+def _int8_operands(y, wq, ws, bias, M: int, K: int):
+    N = wq.shape[0]
+    _want(wq.dtype == torch.int8 and wq.dim() == 2 and wq.shape[1] == K and wq.is_contiguous(), "wq must be contiguous int8 [N, K]")
+    _want(ws.dtype == torch.float32 and ws.numel() == N and ws.is_contiguous(), "ws must be contiguous fp32 [N]")
+    _want(bias is None or (bias.dtype == torch.bfloat16 and bias.numel() == N and bias.is_contiguous()), "bias must be contiguous bf16 [N]")
+    _want(y.dtype in (torch.bfloat16, torch.float32) and y.shape == (M, N) and y.is_contiguous(), "y must be contiguous bf16 or fp32 [M, N]")
+    return N, OUT_F32 if y.dtype == torch.float32 else OUT_BF16
+
+
+def int8_linear_into(y, xq, xs, wq, ws, bias=None, stream=None):
+    """y = xs ws (xq wq^T) + b from int8 codes xq [M, K], wq [N, K] and fp32 scales of
+    each token and output channel (quantize_ex(x, 8, 0), quantize(W, 8, 0)); y bf16 or fp32."""
+    M, K = xq.shape
+    _on(y, xq, xs, wq, ws, bias)
+    _want(xq.dtype == torch.int8 and xq.is_contiguous(), "xq must be contiguous int8 [M, K]")
+    _want(xs.dtype == torch.float32 and xs.numel() == M and xs.is_contiguous(), "xs must be contiguous fp32 [M]")
+    N, out = _int8_operands(y, wq, ws, bias, M, K)
+    _check(lib.wlq_int8_linear(_ptr(xq), _ptr(xs), M, _ptr(wq), _ptr(ws), N, K, _ptr(bias), _ptr(y), out, _stream(stream)))
+    return y
+
+
+def w8a8_workspace(M: int, K: int) -> int:
+    """Workspace bytes of w8a8_linear."""
+    return int(lib.wlq_w8a8_workspace(M, K))
+
+
+def w8a8_linear_into(y, x, wq, ws, bias=None, workspace=None, stream=None):
+    """The W8A8 forward from bf16 x [M, K]: x quantized token by token in the
+    workspace, then y = xs ws (xq wq^T) + b (int8 wq [N, K], fp32 ws [N])."""
+    M, K = x.shape
+    _on(y, x, wq, ws, bias, workspace)
+    _want(x.dtype == torch.bfloat16 and x.is_contiguous(), "x must be contiguous bf16 [M, K]")
+    N, out = _int8_operands(y, wq, ws, bias, M, K)
+    if workspace is None:
+        n = int(lib.wlq_w8a8_workspace(M, K))
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+    ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.wlq_w8a8_linear(_ptr(x), M, _ptr(wq), _ptr(ws), N, K, _ptr(bias), _ptr(y), out, _ptr(workspace), ws_n, _stream(stream)))
+    return y
+
+
+def w8a8_linear(x, wq, ws, bias=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """w8a8_linear_into with a new y [M, N]."""
+    y = torch.empty((x.shape[0], wq.shape[0]), dtype=out_dtype, device=x.device)
+    return w8a8_linear_into(y, x, wq, ws, bias, workspace, stream)
 
 
 def get_status(stream=None) -> int:

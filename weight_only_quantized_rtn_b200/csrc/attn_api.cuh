@@ -94,11 +94,12 @@ wlq_status check_pool(const void* kc, const void* ks, const void* vc, const void
     return WLQ_OK;
 }
 
-// How a call of the decode kernel is cut: row tiles of 8 nt rows, and the
-// splits of a sequence's cached tokens over CTAs.
+// How a call is cut: the kernel, its row tiles (8 nt rows; 256 of the chunk
+// kernel), and the splits of a sequence's cached tokens over CTAs.
 constexpr int kPlanSms = 148;  // the SMs of a B200: plans, and with them workspace sizes, need no device
 
 struct DecPlan {
+    bool chunk = false;
     int nt = 1, row_tiles = 1, splits = 1;
     size_t off_ml = 0, ws = 0;
 };
@@ -107,15 +108,21 @@ DecPlan dec_plan(int64_t tokens, int batch, int max_q, int64_t max_kv, int q_hea
                  int sms) {
     DecPlan p;
     const int64_t rows = static_cast<int64_t>(max_q) * (q_heads / kv_heads);
+    p.chunk = rows > 32;
     p.nt = rows > 8 ? 2 : 1;
-    p.row_tiles = static_cast<int>(cdiv(rows, 8 * p.nt));
+    p.row_tiles = static_cast<int>(cdiv(rows, p.chunk ? 2 * wlq::CH_ROWS : 8 * p.nt));
     int64_t seen = std::max<int64_t>(max_kv, 1);
     if (window > 0) seen = std::min<int64_t>(seen, static_cast<int64_t>(window) + max_q);
-    const int64_t units = cdiv(seen, wlq::DEC_UNIT);
     const int64_t base = static_cast<int64_t>(batch) * kv_heads * p.row_tiles;
+    const int64_t units = cdiv(seen, p.chunk ? wlq::CH_KEYS : wlq::DEC_UNIT);
+    if (p.chunk) {
+        // one CTA an SM: split where the row tiles leave half of them idle, four steps a part at least
+        p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms / base, units / 4, 32})));
+    } else {
     // enough CTAs for four on each SM, but at least two units for each warp of a split
     const int64_t want = cdiv(4ll * sms, base), most = std::max<int64_t>(1, units / (2 * wlq::DEC_WARPS));
     p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, 128})));
+    }
     if (p.splits > 1) {
         const size_t parts = static_cast<size_t>(tokens) * q_heads * p.splits;
         p.off_ml = align256(parts * head_dim * sizeof(float));
@@ -125,11 +132,21 @@ DecPlan dec_plan(int64_t tokens, int batch, int max_q, int64_t max_kv, int q_hea
 }
 
 template <int D>
-wlq_status launch_decode(const wlq::AttnArgs& a, const DecPlan& p, cudaStream_t s) {
+wlq_status launch_attention(const wlq::AttnArgs& a, const DecPlan& p, DeviceInfo* d, cudaStream_t s) {
     const int64_t grid = static_cast<int64_t>(a.B.batch) * a.P.heads * p.row_tiles * p.splits;
     if (grid >= (int64_t(1) << 31)) return fail(WLQ_ERR_SHAPE, "too many queries in one call");
     const unsigned gx = static_cast<unsigned>(grid);
-    cudaError_t e = p.nt == 1 ? launch_k(wlq::kv4_decode_kernel<D, 1>, gx, wlq::DEC_WARPS * 32, 0, s, a)
+    cudaError_t e;
+    if (p.chunk) {
+        const int kid = D == 128 ? 55 : 54;
+        if (!d->smem_set[kid]) {
+            e = cudaFuncSetAttribute(wlq::kv4_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(wlq::ch_smem_bytes<D>()));
+            if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+            d->smem_set[kid] = true;
+        }
+        e = launch_k(wlq::kv4_chunk_kernel<D>, gx, wlq::CH_THREADS, wlq::ch_smem_bytes<D>(), s, a, kDefaultTimeoutNs);
+    } else
+    e = p.nt == 1 ? launch_k(wlq::kv4_decode_kernel<D, 1>, gx, wlq::DEC_WARPS * 32, 0, s, a)
                               : launch_k(wlq::kv4_decode_kernel<D, 2>, gx, wlq::DEC_WARPS * 32, 0, s, a);
     if (e == cudaSuccess && p.splits > 1) {
         const int64_t units = cdiv(static_cast<int64_t>(a.B.batch) * a.B.max_q * a.q_heads, 8);
@@ -305,7 +322,206 @@ wlq_status wlq_kv4_attention(const void* q, int64_t q_stride, int64_t tokens, in
     a.part_o = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.off_ml);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return head_dim == 128 ? launch_decode<128>(a, p, s) : launch_decode<64>(a, p, s);
+    return head_dim == 128 ? launch_attention<128>(a, p, d, s) : launch_attention<64>(a, p, d, s);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// W8A8 Linear
+namespace {
+
+struct I8Plan {
+    bool pair = false;
+    int bn = 16, NT = 0, MT = 0, S = 1, stages = 0;
+    uint32_t b_bytes = 0, stage_bytes = 0;
+    size_t smem = 0;
+};
+
+I8Plan i8_plan(int64_t M, int64_t N, int64_t K) {
+    I8Plan p;
+    const int64_t KB = cdiv(K, 128);
+    const int64_t pairs = kPlanSms / 2, nt2 = cdiv(N, 256), mt256 = cdiv(M, 256);
+    if (nt2 * mt256 * 2 >= pairs) {
+        // even token tiles: the count (a few from the least possible) whose rounds of tiles take the fewest columns
+        int64_t best = -1;
+        for (int64_t t = mt256; t <= mt256 + 3; ++t) {
+            const int64_t bn = cdiv(cdiv(M, t), 32) * 32, tiles = nt2 * cdiv(M, bn);
+            const int64_t cost = cdiv(tiles, pairs) * (bn + 16);  // 16: what a tile costs beside its columns
+            if (best < 0 || cost < best) {
+                best = cost;
+                p.bn = static_cast<int>(bn);
+            }
+        }
+        p.pair = true;
+        p.NT = static_cast<int>(nt2);
+        p.b_bytes = static_cast<uint32_t>(p.bn / 2) * 128u;
+    } else {
+        const int64_t t = cdiv(M, 128);
+        p.bn = static_cast<int>(cdiv(cdiv(M, t), 16) * 16);
+        p.NT = static_cast<int>(cdiv(N, 128));
+        const int64_t tiles = p.NT * t;
+        while (p.S * 2 <= 8 && tiles * p.S * 2 <= kPlanSms && KB >= p.S * 2) p.S *= 2;
+        p.b_bytes = static_cast<uint32_t>(p.bn) * 128u;
+    }
+    p.MT = static_cast<int>(cdiv(M, p.bn));
+    p.stage_bytes = wlq::I8_A_BYTES + p.b_bytes;
+    p.stages = wlq::I8_MAX_STAGES;
+    while (wlq::i8_smem_bytes(p.stages, p.stage_bytes) > kSmemLimit) --p.stages;
+    p.smem = wlq::i8_smem_bytes(p.stages, p.stage_bytes);
+    return p;
+}
+
+template <bool PAIR>
+wlq_status launch_i8(const I8Plan& p, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& ty,
+                     const wlq::I8Args& a, DeviceInfo* d, cudaStream_t s) {
+    auto kern = wlq::int8_gemm_kernel<PAIR>;
+    const int kid = PAIR ? 53 : 52;
+    if (!d->smem_set[kid]) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemLimit));
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+        d->smem_set[kid] = true;
+    }
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    const int csize = PAIR ? 2 : p.S;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(csize);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    // split tiles: one cluster each; else persistent CTAs (pairs)
+    const int clusters = (!PAIR && p.S > 1) ? a.tiles : std::min(a.tiles, d->sms / csize);
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * csize), 1, 1);
+    cfg.blockDim = dim3(wlq::I8_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = csize > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tw, tx, ty, a);
+    return e == cudaSuccess ? WLQ_OK : cuda_fail(e, "int8 gemm launch");
+}
+
+wlq_status check_int8(const void* x, int64_t M, const void* wq, const float* ws, int64_t N, int64_t K, const void* bias,
+                      const void* y, int y_dtype, bool* noop) {
+    *noop = false;
+    if (M < 0 || N < 0) return fail(WLQ_ERR_INVALID_ARG, "M and N must be >= 0");
+    if (K <= 0 || K % 16) return fail(WLQ_ERR_SHAPE, "the int8 Linear needs K a positive multiple of 16");
+    if (K > 131056) return fail(WLQ_ERR_SHAPE, "K above 131056: a 32-bit sum could overflow");
+    if (M > (int64_t(1) << 30) || N > (int64_t(1) << 30)) return fail(WLQ_ERR_SHAPE, "M or N too large");
+    if (y_dtype != WLQ_OUT_BF16 && y_dtype != WLQ_OUT_F32) return fail(WLQ_ERR_INVALID_ARG, "bad y_dtype");
+    if (M == 0 || N == 0) {
+        *noop = true;
+        return WLQ_OK;
+    }
+    if (cdiv(N, 128) * cdiv(M, 16) >= (int64_t(1) << 31)) return fail(WLQ_ERR_SHAPE, "M x N too large");
+    if (!x || !wq || !ws || !y) return fail(WLQ_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(x) || !aligned16(wq) || !aligned4(ws) || !aligned2(bias) || !aligned4(y))
+        return fail(WLQ_ERR_ALIGN, "x and wq must be 16-byte aligned, ws and y 4-byte, bias 2-byte");
+    return WLQ_OK;
+}
+
+wlq_status int8_linear_impl(const void* xq, const float* xs, int64_t M, const void* wq, const float* ws, int64_t N, int64_t K,
+                            const void* bias, void* y, int y_dtype, DeviceInfo* d, cudaStream_t s) {
+    const I8Plan p = i8_plan(M, N, K);
+    CUtensorMap tw, tx, ty;
+    std::memset(&ty, 0, sizeof ty);
+    wlq_status st;
+    if ((st = make_map_u8(&tw, wq, N, K, 128)) != WLQ_OK) return st;
+    if ((st = make_map_u8(&tx, xq, M, K, p.pair ? p.bn / 2 : p.bn)) != WLQ_OK) return st;
+    wlq::I8Args a;
+    std::memset(&a, 0, sizeof a);
+    a.xs = xs;
+    a.ws = ws;
+    a.bias = static_cast<const uint16_t*>(bias);
+    a.y = y;
+    a.M = static_cast<int>(M);
+    a.N = static_cast<int>(N);
+    a.NT = p.NT;
+    a.KB = static_cast<int>(cdiv(K, 128));
+    a.tiles = p.NT * p.MT;
+    a.bn = p.bn;
+    a.S = p.S;
+    a.stages = p.stages;
+    a.b_bytes = p.b_bytes;
+    a.stage_bytes = p.stage_bytes;
+    a.acc2 = p.pair ? 256u : 128u;
+    a.tmem_cols = 2 * a.acc2;
+    a.y_f32 = (y_dtype == WLQ_OUT_F32) ? 1 : 0;
+    const size_t esize = a.y_f32 ? 4 : 2;
+    if (p.S == 1 && aligned16(y) && (static_cast<size_t>(N) * esize) % 16 == 0) {
+        EncodeTiledFn fn = encode_fn();
+        if (!fn) return fail(WLQ_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(N) * esize};
+        const cuuint32_t box[2] = {32, 16};
+        const cuuint32_t estr[2] = {1, 1};
+        const CUresult cr = fn(&ty, a.y_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, y, dims, strides, box,
+                               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (cr != CUDA_SUCCESS) return fail(WLQ_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(cr));
+        a.tma_store = 1;
+    }
+    a.timeout_ns = kDefaultTimeoutNs;
+    return p.pair ? launch_i8<true>(p, tw, tx, ty, a, d, s) : launch_i8<false>(p, tw, tx, ty, a, d, s);
+}
+
+wlq_status launch_quantize_tokens(const void* x, int64_t M, int64_t K, int8_t* codes, float* scales, DeviceInfo* d, cudaStream_t s) {
+    const int per = static_cast<int>(cdiv(K / 8, 256));
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(M, static_cast<int64_t>(d->sms) * 8));
+    const uint16_t* xb = static_cast<const uint16_t*>(x);
+    const int m = static_cast<int>(M), k = static_cast<int>(K);
+    cudaError_t e;
+    if (per <= 1) e = launch_k(wlq::quantize_tokens_kernel<1>, grid, 256, 0, s, xb, m, k, codes, scales);
+    else if (per <= 2) e = launch_k(wlq::quantize_tokens_kernel<2>, grid, 256, 0, s, xb, m, k, codes, scales);
+    else if (per <= 4) e = launch_k(wlq::quantize_tokens_kernel<4>, grid, 256, 0, s, xb, m, k, codes, scales);
+    else if (per <= 8) e = launch_k(wlq::quantize_tokens_kernel<8>, grid, 256, 0, s, xb, m, k, codes, scales);
+    else if (per <= 16) e = launch_k(wlq::quantize_tokens_kernel<16>, grid, 256, 0, s, xb, m, k, codes, scales);
+    else e = launch_k(wlq::quantize_tokens_kernel<0>, grid, 256, 0, s, xb, m, k, codes, scales);
+    return e == cudaSuccess ? WLQ_OK : cuda_fail(e, "quantize_tokens launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+wlq_status wlq_int8_linear(const void* xq, const float* xs, int64_t M, const void* wq, const float* ws, int64_t N,
+                           int64_t K, const void* bias, void* y, int y_dtype, void* stream) {
+    bool noop = false;
+    wlq_status st = check_int8(xq, M, wq, ws, N, K, bias, y, y_dtype, &noop);
+    if (st != WLQ_OK || noop) return st;
+    if (!xs) return fail(WLQ_ERR_INVALID_ARG, "null pointer");
+    if (!aligned4(xs)) return fail(WLQ_ERR_ALIGN, "xs must be 4-byte aligned");
+    int dev;
+    DeviceInfo* d;
+    if ((st = current_device(&dev, &d)) != WLQ_OK) return st;
+    return int8_linear_impl(xq, xs, M, wq, ws, N, K, bias, y, y_dtype, d, static_cast<cudaStream_t>(stream));
+}
+
+size_t wlq_w8a8_workspace(int64_t M, int64_t K) {
+    if (M <= 0 || K <= 0 || K % 16) return 0;
+    return align256(static_cast<size_t>(M) * static_cast<size_t>(K)) + align256(static_cast<size_t>(M) * 4);
+}
+
+wlq_status wlq_w8a8_linear(const void* x, int64_t M, const void* wq, const float* ws, int64_t N, int64_t K,
+                           const void* bias, void* y, int y_dtype, void* workspace, size_t ws_bytes, void* stream) {
+    bool noop = false;
+    wlq_status st = check_int8(x, M, wq, ws, N, K, bias, y, y_dtype, &noop);
+    if (st != WLQ_OK || noop) return st;
+    const size_t need = wlq_w8a8_workspace(M, K);
+    if (!workspace || ws_bytes < need)
+        return fail(WLQ_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace ? ws_bytes : size_t(0));
+    if (!aligned16(workspace)) return fail(WLQ_ERR_ALIGN, "workspace must be 16-byte aligned");
+    int dev;
+    DeviceInfo* d;
+    if ((st = current_device(&dev, &d)) != WLQ_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int8_t* codes = static_cast<int8_t*>(workspace);
+    float* scales = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(static_cast<size_t>(M) * static_cast<size_t>(K)));
+    if ((st = launch_quantize_tokens(x, M, K, codes, scales, d, s)) != WLQ_OK) return st;
+    return int8_linear_impl(codes, scales, M, wq, ws, N, K, bias, y, y_dtype, d, s);
 }
 
 }  // extern "C"

@@ -1,0 +1,475 @@
+// kv4_chunk.cuh -- attention of many queries (prompts, chunks of video tokens)
+// over the paged 4-bit cache, on the tcgen05 tensor cores.
+//
+// A CTA takes 256 rows (tokens x the query heads that share a cache head) as
+// two tiles of 128 and walks the cached tokens in tiles of 128:
+//   S_t = Q_t K^T   (shared memory x shared memory, fp32 in tensor memory)
+//   P_t = exp2(S_t c - m)   as fp16 over S_t's own tensor-memory columns
+//   O_t += P_t V    (tensor memory x shared memory)
+// Roles: two warpgroups of softmax (a thread owns a row: no shuffles), one of
+// dequantisation, one warp that issues MMAs.  While one tile's weights are
+// computed the tensor cores work on the other: the issue order is PV_0(j),
+// QK_0(j+1), PV_1(j), QK_1(j+1), and since they execute in that order S_t(j+1)
+// may overwrite the columns PV_t(j) has read.
+//
+// K and V tiles are written by the dequantisation warps as fp16 code * scale
+// (one rounding) in one layout: rows of 64 inputs (128 bytes, 128-byte
+// swizzle), which is the K-major operand of the scores and the MN-major operand
+// of the outputs.  A lane takes 16 bytes of codes (32 inputs, one scale); the
+// order in which it stores its four 16-byte results alternates with the
+// row half, so a quarter warp's stores cover all banks.
+//
+// The running maximum is lazy, as in kv4_decode.cuh: weights are computed with
+// the m at hand while the scores are still in tensor memory, and only when one
+// passes 2^8 is m moved, the tile computed again and O_t rescaled.
+//
+// Bound: the exponentials (16 a clock and SM) and the tensor cores, which take
+// the same time for D = 128: 4 x 512 clocks of MMAs and 2 x 1024 of
+// exponentials for 256 rows x 128 tokens.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include "kv4_decode.cuh"
+#include "kvcache.cuh"
+#include "nvfp4.cuh"
+#include "ptx.cuh"
+
+namespace wlq {
+
+constexpr int CH_ROWS = 128;  // rows of a tile
+constexpr int CH_KEYS = 128;  // cached tokens of a step
+constexpr int CH_THREADS = 512;  // two softmax warpgroups, one of dequantisation, one whose first warp issues MMAs
+constexpr int CH_STAGES = 2;
+// Registers a thread of each role, moved after the start: 2 x 184 + 104 + 40 = 4 x 128, what the block was launched with.
+constexpr int CH_REGS_SOFTMAX = 184, CH_REGS_DEQUANT = 104, CH_REGS_MMA = 40;
+static_assert(2 * CH_REGS_SOFTMAX + CH_REGS_DEQUANT + CH_REGS_MMA == 4 * 128, "register shares");
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+template <int D>
+__host__ __device__ constexpr uint32_t ch_tile_bytes() { return 128u * D * 2u; }
+template <int D>
+__host__ __device__ constexpr size_t ch_smem_bytes() { return 1024 + (2 + 2 * CH_STAGES) * ch_tile_bytes<D>() + 256; }
+
+// Shared-memory descriptor of an MN-major operand with the 128-byte swizzle:
+// rows of 64 MN values (128 bytes), eight of them (1024 bytes) a swizzle atom,
+// the next 64 MN values `chunk` bytes away.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t chunk) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(chunk >> 4) << 16;  // leading byte offset: the next 64 MN values
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;   // stride byte offset: the next 8 rows of K
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+// Cached-token steps [jb, je) of a row tile within the CTA's split.
+struct ChRange {
+    int jb, je;
+    __device__ __forceinline__ bool at(int j) const { return j >= jb && j < je; }
+};
+
+template <int D>
+__global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs a, uint64_t timeout_ns) {
+    constexpr uint32_t TILE = ch_tile_bytes<D>();
+    constexpr uint32_t HALF = 128u * 128u;  // one 64-input column block of a tile
+    extern __shared__ uint8_t ch_smem_raw[];
+    uint8_t* base = ch_smem_raw + ((1024u - (smem_u32(ch_smem_raw) & 1023u)) & 1023u);
+    uint8_t* sq = base;
+    uint8_t* sk = base + 2 * TILE;
+    uint8_t* sv = sk + CH_STAGES * TILE;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sv + CH_STAGES * TILE);
+    uint64_t* kfull = bars;                  // [2]
+    uint64_t* kempty = bars + 2;             // [2]
+    uint64_t* vfull = bars + 4;              // [2]
+    uint64_t* vempty = bars + 6;             // [2]
+    uint64_t* sfull = bars + 8;              // [2] scores of tile t are in tensor memory
+    uint64_t* pfull = bars + 10;             // [2] weights of tile t are
+    uint64_t* pvdone = bars + 12;            // [2] O_t has them
+    uint64_t* qfull = bars + 14;
+    uint64_t* drain = bars + 15;
+    uint32_t* pbad = reinterpret_cast<uint32_t*>(bars + 16);  // [4 steps][4 warps] a bit for each 16 tokens whose page is out of range
+    uint32_t* tmem_slot = pbad + 16;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dependency_sync();
+    // late row tiles (the longest, where causal) first
+    int idx = blockIdx.x;
+    const int split = idx % a.splits;
+    idx /= a.splits;
+    const int h = idx % a.P.heads;
+    idx /= a.P.heads;
+    const int b = idx % a.B.batch, rt = a.row_tiles - 1 - idx / a.B.batch;
+    const int64_t r0 = a.B.cu[b], r1 = a.B.cu[b + 1];
+    const int kv = a.B.kv_len[b];
+    const KvRange seq = kv_sequence(r0, r1, kv, a.B.max_q, a.B.tokens);
+    if (seq != KV_OK) {
+        if (seq == KV_BAD && threadIdx.x == 0) raise_error(ERRBIT_INDEX);
+        return;
+    }
+    const int n = static_cast<int>(r1 - r0), rows = n * a.share, row0 = rt * 2 * CH_ROWS;
+    if (row0 >= rows) return;
+
+    ChRange R[2];
+    int j0, j1;
+    {
+        int lo, hi, unused;
+        seen_range(a, kv - n + row0 / a.share, kv, lo, unused);
+        seen_range(a, kv - n + (min(rows, row0 + 2 * CH_ROWS) - 1) / a.share, kv, unused, hi);
+        const int u0 = lo / CH_KEYS, u1 = (hi + CH_KEYS - 1) / CH_KEYS, units = max(0, u1 - u0);
+        j0 = u0 + static_cast<int>(static_cast<int64_t>(units) * split / a.splits);
+        j1 = u0 + static_cast<int>(static_cast<int64_t>(units) * (split + 1) / a.splits);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int f = row0 + t * CH_ROWS, l = min(rows, f + CH_ROWS) - 1;
+            R[t].jb = R[t].je = j1;
+            if (f < rows) {
+                seen_range(a, kv - n + f / a.share, kv, lo, unused);
+                seen_range(a, kv - n + l / a.share, kv, unused, hi);
+                R[t].jb = max(j0, lo / CH_KEYS);
+                R[t].je = max(R[t].jb, min(j1, (hi + CH_KEYS - 1) / CH_KEYS));
+            }
+        }
+    }
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&kfull[i], 4);
+            mbar_init(&kempty[i], 1);
+            mbar_init(&vfull[i], 4);
+            mbar_init(&vempty[i], 1);
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pfull[i], 4);
+            mbar_init(&pvdone[i], 1);
+        }
+        mbar_init(qfull, 8);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 12) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ softmax
+        regs_inc<CH_REGS_SOFTMAX>();
+        const int t = warp >> 2, q4 = warp & 3;
+        const int row = row0 + t * CH_ROWS + q4 * 32 + lane;
+        const bool live = row < rows;
+        const int crow = min(row, rows - 1);
+        const int64_t token = r0 + crow / a.share;
+        const int head = h * a.share + crow % a.share;
+        float c;  // scores to powers of two
+        {
+            // the row's queries: fp16 of q 2^e, into the tile's swizzled rows
+            const uint4* p = reinterpret_cast<const uint4*>(a.q + token * a.q_stride + static_cast<int64_t>(head) * D);
+            uint4 raw[D / 8];
+            uint32_t m2 = 0;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                raw[i] = live ? p[i] : make_uint4(0u, 0u, 0u, 0u);
+                m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(raw[i].x & 0x7FFF7FFFu, raw[i].y & 0x7FFF7FFFu),
+                                           __vmaxu2(raw[i].z & 0x7FFF7FFFu, raw[i].w & 0x7FFF7FFFu)));
+            }
+            const int e = row_exponent(max(m2 & 0xFFFFu, m2 >> 16));
+            const float f = pow2f(e);
+            c = a.scale_log2 * pow2f(-e);
+            const int r = q4 * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    o[k] = h2_bits(__floats2half2_rn(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f));
+                uint8_t* dst = sq + t * TILE + (i / 8) * HALF + r * 128 + (((i & 7) ^ (r & 7)) << 4);
+                *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qfull);
+        }
+        int lo, hi;
+        seen_range(a, kv - n + crow / a.share, kv, lo, hi);
+        const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
+        const uint32_t s_t = tmem + lane_base + t * 128, o_t = tmem + lane_base + 256 + t * 128;
+        float m = -INFINITY, l = 0.0f;
+        int done = 0;  // steps of this tile so far
+        bool ok = true;
+        const ChRange Rt = t ? R[1] : R[0];
+        for (int j = Rt.jb; j < Rt.je; ++j, ++done) {
+            if (!warp_wait(&sfull[t], done & 1, timeout_ns, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const int k0 = j * CH_KEYS;
+            // the step's slot is written again four steps later, when this tile's weights have been used
+            const uint4 bad4 = *reinterpret_cast<const uint4*>(pbad + (j & 3) * 4);
+            const uint32_t bad = bad4.x | bad4.y | bad4.z | bad4.w;
+            const bool inside = __all_sync(0xffffffffu, k0 >= lo && k0 + CH_KEYS <= hi && bad == 0);
+            uint32_t pk[64];
+            float ls;
+            for (int again = 0;; ++again) {
+                const float base_m = m == -INFINITY ? 0.0f : m;
+                float top = -INFINITY;
+                float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch) {
+                    uint32_t v[16];
+                    tmem_ld16(s_t + 16 * ch, v);
+                    tmem_wait_ld_pin(v);
+                    if (!inside) {
+                        const bool page = !(bad >> ch & 1u);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int key = k0 + 16 * ch + i;
+                            if (key < lo || key >= hi || !page) v[i] = 0xFF800000u;
+                            else v[i] = __float_as_uint(__uint_as_float(v[i]) * c);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * c);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float x0 = __uint_as_float(v[i]) - base_m, x1 = __uint_as_float(v[i + 1]) - base_m;
+                        top = fmaxf(top, fmaxf(x0, x1));
+                        const float p0 = ex2(x0), p1 = ex2(x1);
+                        sum[0] += p0;
+                        sum[1] += p1;
+                        pk[8 * ch + i / 2] = h2_bits(__floats2half2_rn(p0, p1));
+                    }
+                }
+                ls = sum[0] + sum[1];
+                const bool move = m == -INFINITY ? top > -INFINITY : top > ATT_LAZY;
+                if (again || !__any_sync(0xffffffffu, move)) break;
+                // move the maximum, rescale what there is, compute the step again
+                const float mn = move ? base_m + top : m;
+                const float f = move ? ex2(m - mn) : 1.0f;  // 0 from -inf
+                m = mn;
+                l *= f;
+                if (done > 0) {
+                    if (!warp_wait(&pvdone[t], (done - 1) & 1, timeout_ns, abort_flag)) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll
+                    for (int d = 0; d < D; d += 16) {
+                        uint32_t v[16];
+                        tmem_ld16(o_t + d, v);
+                        tmem_wait_ld_pin(v);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                        tmem_st16(o_t + d, v);
+                    }
+                    tmem_wait_st();
+                }
+            }
+            if (!ok) break;
+            l += ls;
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+                uint32_t v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = pk[16 * ch + i];
+                tmem_st16(s_t + 16 * ch, v);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[t]);
+        }
+        // the row's result
+        if (ok && done > 0) ok = warp_wait(&pvdone[t], (done - 1) & 1, timeout_ns, abort_flag);
+        if (ok) {
+            tc_fence_after();
+            const int64_t head_row = token * a.q_heads + head;
+            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+#pragma unroll
+            for (int d = 0; d < D; d += 16) {
+                uint32_t v[16];
+                if (done > 0) {
+                    tmem_ld16(o_t + d, v);
+                    tmem_wait_ld_pin(v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = 0;
+                }
+                if (live && a.splits == 1) {
+                    uint32_t o[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+                        o[i] = *reinterpret_cast<const uint32_t*>(&y);
+                    }
+                    uint4* dst = reinterpret_cast<uint4*>(a.out + head_row * D + d);
+                    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                } else if (live) {
+                    uint4* dst = reinterpret_cast<uint4*>(a.part_o + (head_row * a.splits + split) * D + d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                }
+                __syncwarp();
+            }
+            if (live) {
+                if (a.splits > 1) a.part_ml[head_row * a.splits + split] = make_float2(m, l);
+                else if (a.lse) a.lse[head_row] = l > 0.0f ? (m + __log2f(l)) * 0.6931471805599453f : (l == 0.0f ? -INFINITY : l);
+            }
+            tc_fence_before();
+        }
+    } else if (warp < 12) {
+        // ----------------------------------------------------- dequantisation
+        regs_dec<CH_REGS_DEQUANT>();
+        constexpr int CPT = D / 32;           // 16-byte pieces of a token's codes
+        constexpr int TOK = 128 / CPT;        // tokens the 128 threads take at once
+        constexpr int REP = 128 / TOK;        // pieces a thread has of a tile
+        const int i = threadIdx.x - 256, piece = i % CPT, tk = i / CPT;
+        const int lg = a.P.lg_group, gpr = D >> lg, grp = (piece * 32) >> lg;
+        int page[REP];
+        uint4 kw[REP], vw[REP];
+        __half ks[REP], vs[REP];
+        auto pages = [&](int j) {
+#pragma unroll
+            for (int r = 0; r < REP; ++r) {
+                const int tok = j * CH_KEYS + tk + r * TOK;
+                page[r] = -1;
+                if (j < j1 && tok < kv) {
+                    const int64_t e = tok >> a.P.page_shift;
+                    if (e < a.B.table_stride) page[r] = a.B.table[b * a.B.table_stride + e];
+                    if (!kv_page_ok(page[r], a.P.pages)) {
+                        raise_error(ERRBIT_INDEX);
+                        page[r] = -1;
+                    }
+                }
+            }
+        };
+        auto load = [&](int j) {  // codes and scales of step j (0 where there is no token)
+#pragma unroll
+            for (int r = 0; r < REP; ++r) {
+                kw[r] = vw[r] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+                ks[r] = vs[r] = __float2half_rn(0.0f);
+                if (page[r] >= 0) {
+                    const int place = (j * CH_KEYS + tk + r * TOK) & ((1 << a.P.page_shift) - 1);
+                    const int64_t row = ((static_cast<int64_t>(page[r]) * a.P.heads + h) << a.P.page_shift) + place;
+                    kw[r] = __ldg(reinterpret_cast<const uint4*>(a.P.k + row * (D / 2)) + piece);
+                    vw[r] = __ldg(reinterpret_cast<const uint4*>(a.P.v + row * (D / 2)) + piece);
+                    ks[r] = a.P.ks[row * gpr + grp];
+                    vs[r] = a.P.vs[row * gpr + grp];
+                }
+            }
+        };
+        auto put = [&](uint8_t* tile, const uint4 (&w)[REP], const __half (&s)[REP]) {
+#pragma unroll
+            for (int r = 0; r < REP; ++r) {
+                const int tok = tk + r * TOK;
+                const uint32_t x[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+                const __half2 s2 = __half2half2(s[r]);
+                uint8_t* rowp = tile + (piece / 2) * HALF + tok * 128;
+                const bool odd = CPT == 4 && (piece & 2);  // the other column block: another store order
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t o[4];
+                    nibbles_f16(odd ? x[k ^ 2] : x[k], s2, o);
+                    const int unit = (piece & 1) * 4 + (odd ? (k ^ 2) : k);
+                    *reinterpret_cast<uint4*>(rowp + ((unit ^ (tok & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+            fence_proxy_async();
+            __syncwarp();
+        };
+        pages(j0);
+        if (j0 < j1) load(j0);
+        for (int j = j0, it = 0; j < j1; ++j, ++it) {
+            const int st = it & 1, ph = (it >> 1) & 1;
+            uint32_t bad = 0;  // 16-token pieces with a token whose page is out of range
+#pragma unroll
+            for (int r = 0; r < REP; ++r)
+                if (page[r] < 0 && j * CH_KEYS + tk + r * TOK < kv) bad |= 1u << ((tk + r * TOK) >> 4);
+            bad = __reduce_or_sync(0xffffffffu, bad);
+            if (!warp_wait(&kempty[st], ph ^ 1, timeout_ns, abort_flag)) break;
+            if (lane == 0) pbad[(j & 3) * 4 + warp - 8] = bad;
+            put(sk + st * TILE, kw, ks);
+            if (lane == 0) mbar_arrive(&kfull[st]);
+            if (!warp_wait(&vempty[st], ph ^ 1, timeout_ns, abort_flag)) break;
+            put(sv + st * TILE, vw, vs);
+            if (lane == 0) mbar_arrive(&vfull[st]);
+            pages(j + 1);
+            if (j + 1 < j1) load(j + 1);
+        }
+    } else {
+        // ---------------------------------------------------------------- MMAs
+        regs_dec<CH_REGS_MMA>();
+        if (warp == 12 && lane == 0) {
+        constexpr uint32_t id_s = idesc_f16(0, 128, CH_KEYS);
+        constexpr uint32_t id_o = idesc_f16(0, 128, D) | (1u << 16);  // B is MN-major
+        int cnt[2] = {0, 0};  // weight steps of each tile so far
+        bool ok = nv_wait(qfull, 0, timeout_ns, abort_flag);
+        auto scores = [&](int t, int j, int it) {  // S_t = Q_t K_j^T
+            const uint32_t qa = smem_u32(sq + t * TILE), ka = smem_u32(sk + (it & 1) * TILE);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+                mma_ss(tmem + t * 128, smem_desc_sw128(qa + (k / 4) * HALF) + 2 * (k % 4), smem_desc_sw128(ka + (k / 4) * HALF) + 2 * (k % 4),
+                       id_s, k > 0 ? 1u : 0u);
+            mma_commit(&sfull[t]);
+        };
+        auto outputs = [&](int t, int j, int it) {  // O_t += P_t V_j
+            const uint64_t vd = smem_desc_mn_sw128(smem_u32(sv + (it & 1) * TILE), HALF);
+#pragma unroll
+            for (int k = 0; k < CH_KEYS / 16; ++k)
+                mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * k, vd + static_cast<uint64_t>(k * 2048 / 16), id_o, (cnt[t] > 0 || k > 0) ? 1u : 0u);
+            mma_commit(&pvdone[t]);
+            ++cnt[t];
+        };
+        if (ok && j0 < j1) {
+            ok = nv_wait(&kfull[0], 0, timeout_ns, abort_flag);
+            if (ok) {
+                tc_fence_after();
+                for (int t = 0; t < 2; ++t)
+                    if (R[t].at(j0)) scores(t, j0, 0);
+                mma_commit(&kempty[0]);
+            }
+        }
+        for (int j = j0, it = 0; ok && j < j1; ++j, ++it) {
+            const int st = it & 1;
+            if (!(ok = nv_wait(&vfull[st], (it >> 1) & 1, timeout_ns, abort_flag))) break;
+            const bool more = j + 1 < j1;
+            bool knext = false;
+            for (int t = 0; t < 2 && ok; ++t) {
+                if (R[t].at(j)) {
+                    if (!(ok = nv_wait(&pfull[t], cnt[t] & 1, timeout_ns, abort_flag))) break;
+                    tc_fence_after();
+                    outputs(t, j, it);
+                }
+                if (t == 1) mma_commit(&vempty[st]);
+                if (more) {
+                    if (!knext) {
+                        if (!(ok = nv_wait(&kfull[st ^ 1], ((it + 1) >> 1) & 1, timeout_ns, abort_flag))) break;
+                        tc_fence_after();
+                        knext = true;
+                    }
+                    if (R[t].at(j + 1)) scores(t, j + 1, it + 1);
+                    if (t == 1) mma_commit(&kempty[st ^ 1]);
+                }
+            }
+        }
+        // every MMA issued has completed before tensor memory is freed
+        mma_commit(drain);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < timeout_ns) {
+        }
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace wlq

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32) kv4_decode_kernel(const AttnAr
     if (row0 >= rows) return;
     const int row_last = min(rows, row0 + 8 * NT) - 1;
     // what any row of the tile sees, what all of them see
-    int lo, hi, lo_all, hi_all, x0, x1;
+    int lo, hi, lo_all, hi_all;
     seen_range(a, kv - n + row0 / a.share, kv, lo, hi_all);
     seen_range(a, kv - n + row_last / a.share, kv, lo_all, hi);
     const int u0 = lo / DEC_UNIT, u1 = (hi + DEC_UNIT - 1) / DEC_UNIT, units = max(0, u1 - u0);

@@ -80,6 +80,27 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
     }
 }
 
+// The whole warp waits (each lane acquires for itself); lane 0 decides to give up.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag) {
+    uint64_t t0 = 0;
+    for (uint32_t spin = 0;; ++spin) {
+        const bool ready = mbar_try_wait(bar, parity);
+        if (__all_sync(0xffffffffu, ready)) return true;
+        int give_up = 0;
+        if ((threadIdx.x & 31) == 0 && (spin & 255) == 255) {
+            if (t0 == 0) t0 = globaltimer_ns();
+            if (*abort_flag) {
+                give_up = 1;
+            } else if (globaltimer_ns() - t0 > timeout_ns) {
+                raise_error(ERRBIT_TIMEOUT);
+                *abort_flag = 1;
+                give_up = 1;
+            }
+        }
+        if (__shfl_sync(0xffffffffu, give_up, 0)) return false;
+    }
+}
+
 // -------------------------------------------------------------- TMA / bulk
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
                                             int32_t c0, int32_t c1) {

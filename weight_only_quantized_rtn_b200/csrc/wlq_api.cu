@@ -27,6 +27,8 @@
 #include "nvfp4.cuh"
 #include "kvcache.cuh"
 #include "kv4_decode.cuh"
+#include "kv4_chunk.cuh"
+#include "int8_gemm.cuh"
 
 namespace {
 
