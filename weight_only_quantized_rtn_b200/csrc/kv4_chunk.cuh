@@ -19,9 +19,9 @@
 // order in which it stores its four 16-byte results alternates with the
 // row half, so a quarter warp's stores cover all banks.
 //
-// The running maximum is lazy, as in kv4_decode.cuh: weights are computed with
-// the m at hand while the scores are still in tensor memory, and only when one
-// passes 2^8 is m moved, the tile computed again and O_t rescaled.
+// A thread holds its row's 128 scores in registers: maximum, weights and their
+// sum are taken from there.  The running maximum is lazy, as in kv4_decode.cuh:
+// O_t is rescaled only when a step's maximum passes it by more than 8 (log2).
 //
 // Bound: the exponentials (16 a clock and SM) and the tensor cores, which take
 // the same time for D = 128: 4 x 512 clocks of MMAs and 2 x 1024 of
@@ -41,8 +41,8 @@ constexpr int CH_ROWS = 128;  // rows of a tile
 constexpr int CH_KEYS = 128;  // cached tokens of a step
 constexpr int CH_THREADS = 512;  // two softmax warpgroups, one of dequantisation, one whose first warp issues MMAs
 constexpr int CH_STAGES = 2;
-// Registers a thread of each role, moved after the start: 2 x 184 + 104 + 40 = 4 x 128, what the block was launched with.
-constexpr int CH_REGS_SOFTMAX = 184, CH_REGS_DEQUANT = 104, CH_REGS_MMA = 40;
+// Registers a thread of each role, moved after the start: 2 x 176 + 112 + 48 = 4 x 128, what the block was launched with.
+constexpr int CH_REGS_SOFTMAX = 176, CH_REGS_DEQUANT = 112, CH_REGS_MMA = 48;
 static_assert(2 * CH_REGS_SOFTMAX + CH_REGS_DEQUANT + CH_REGS_MMA == 4 * 128, "register shares");
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -180,8 +180,14 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
                                            __vmaxu2(raw[i].z & 0x7FFF7FFFu, raw[i].w & 0x7FFF7FFFu)));
             }
             const int e = row_exponent(max(m2 & 0xFFFFu, m2 >> 16));
-            const float f = pow2f(e);
-            c = a.scale_log2 * pow2f(-e);
+            // a negative scale turns the queries round; a factor of zero makes them zero (and stays
+            // positive: unseen scores are -inf before it is applied)
+            float f = a.scale_log2 < 0.0f ? -pow2f(e) : pow2f(e);
+            c = fabsf(a.scale_log2) * pow2f(-e);
+            if (c == 0.0f) {
+                f = 0.0f;
+                c = 1.0f;
+            }
             const int r = q4 * 32 + lane;
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
@@ -213,71 +219,65 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
             const uint4 bad4 = *reinterpret_cast<const uint4*>(pbad + (j & 3) * 4);
             const uint32_t bad = bad4.x | bad4.y | bad4.z | bad4.w;
             const bool inside = __all_sync(0xffffffffu, k0 >= lo && k0 + CH_KEYS <= hi && bad == 0);
-            uint32_t pk[64];
-            float ls;
-            for (int again = 0;; ++again) {
-                const float base_m = m == -INFINITY ? 0.0f : m;
-                float top = -INFINITY;
-                float sum[2] = {0.0f, 0.0f};
+            uint32_t v[8][16];
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) tmem_ld16(s_t + 16 * ch, v[ch]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) reg_pin(v[ch]);
+            if (!inside) {
 #pragma unroll
                 for (int ch = 0; ch < 8; ++ch) {
-                    uint32_t v[16];
-                    tmem_ld16(s_t + 16 * ch, v);
-                    tmem_wait_ld_pin(v);
-                    if (!inside) {
-                        const bool page = !(bad >> ch & 1u);
+                    // keys of this piece from `first` to `last` are seen
+                    const int first = lo - k0 - 16 * ch, last = (bad >> ch & 1u) ? 0 : hi - k0 - 16 * ch;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int key = k0 + 16 * ch + i;
-                            if (key < lo || key >= hi || !page) v[i] = 0xFF800000u;
-                            else v[i] = __float_as_uint(__uint_as_float(v[i]) * c);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * c);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float x0 = __uint_as_float(v[i]) - base_m, x1 = __uint_as_float(v[i + 1]) - base_m;
-                        top = fmaxf(top, fmaxf(x0, x1));
-                        const float p0 = ex2(x0), p1 = ex2(x1);
-                        sum[0] += p0;
-                        sum[1] += p1;
-                        pk[8 * ch + i / 2] = h2_bits(__floats2half2_rn(p0, p1));
-                    }
+                    for (int i = 0; i < 16; ++i)
+                        if (i < first || i >= last) v[ch][i] = 0xFF800000u;
                 }
-                ls = sum[0] + sum[1];
-                const bool move = m == -INFINITY ? top > -INFINITY : top > ATT_LAZY;
-                if (again || !__any_sync(0xffffffffu, move)) break;
-                // move the maximum, rescale what there is, compute the step again
-                const float mn = move ? base_m + top : m;
-                const float f = move ? ex2(m - mn) : 1.0f;  // 0 from -inf
-                m = mn;
+            }
+            float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch)
+#pragma unroll
+                for (int i = 0; i < 16; i += 2)
+                    top4[(i / 2) & 3] = fmaxf(top4[(i / 2) & 3], fmaxf(__uint_as_float(v[ch][i]), __uint_as_float(v[ch][i + 1])));
+            const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * c;  // c > 0
+            const bool move = top > m + ATT_LAZY;  // also from -inf
+            if (__any_sync(0xffffffffu, move)) {
+                const float f = move ? ex2(m - top) : 1.0f;  // 0 from -inf
+                if (move) m = top;
                 l *= f;
                 if (done > 0) {
                     if (!warp_wait(&pvdone[t], (done - 1) & 1, timeout_ns, abort_flag)) { ok = false; break; }
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int d = 0; d < D; d += 16) {
-                        uint32_t v[16];
-                        tmem_ld16(o_t + d, v);
-                        tmem_wait_ld_pin(v);
+                        uint32_t o[16];
+                        tmem_ld16(o_t + d, o);
+                        tmem_wait_ld_pin(o);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                        tmem_st16(o_t + d, v);
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st16(o_t + d, o);
                     }
                     tmem_wait_st();
                 }
             }
-            if (!ok) break;
-            l += ls;
+            const float nm = m == -INFINITY ? 0.0f : -m;  // nothing seen yet: every score is -inf
+            float sum[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch) {
-                uint32_t v[16];
+                uint32_t pk[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = pk[16 * ch + i];
-                tmem_st16(s_t + 16 * ch, v);
+                for (int i = 0; i < 16; ++i) {
+                    const float p0 = ex2(fmaf(__uint_as_float(v[2 * ch + i / 8][(2 * i) & 15]), c, nm));
+                    const float p1 = ex2(fmaf(__uint_as_float(v[2 * ch + i / 8][(2 * i + 1) & 15]), c, nm));
+                    sum[0] += p0;
+                    sum[1] += p1;
+                    pk[i] = h2_bits(__floats2half2_rn(p0, p1));
+                }
+                tmem_st16(s_t + 16 * ch, pk);
             }
+            l += sum[0] + sum[1];
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -330,36 +330,35 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
         constexpr int REP = 128 / TOK;        // pieces a thread has of a tile
         const int i = threadIdx.x - 256, piece = i % CPT, tk = i / CPT;
         const int lg = a.P.lg_group, gpr = D >> lg, grp = (piece * 32) >> lg;
-        int page[REP];
+        int page[REP], next[REP];  // this step's pages (-1: none or out of range), the next one's
         uint4 kw[REP], vw[REP];
         __half ks[REP], vs[REP];
-        auto pages = [&](int j) {
+        auto pages = [&](int j, int (&pg)[REP]) {
 #pragma unroll
             for (int r = 0; r < REP; ++r) {
                 const int tok = j * CH_KEYS + tk + r * TOK;
-                page[r] = -1;
+                pg[r] = -1;
                 if (j < j1 && tok < kv) {
                     const int64_t e = tok >> a.P.page_shift;
-                    if (e < a.B.table_stride) page[r] = a.B.table[b * a.B.table_stride + e];
-                    if (!kv_page_ok(page[r], a.P.pages)) {
+                    if (e < a.B.table_stride) pg[r] = a.B.table[b * a.B.table_stride + e];
+                    if (!kv_page_ok(pg[r], a.P.pages)) {
                         raise_error(ERRBIT_INDEX);
-                        page[r] = -1;
+                        pg[r] = -1;
                     }
                 }
             }
         };
-        auto load = [&](int j) {  // codes and scales of step j (0 where there is no token)
+        // codes and scales of step j (zeros where there is no token)
+        auto load = [&](int j, const uint8_t* codes, const __half* scales, const int (&pg)[REP], uint4 (&w)[REP], __half (&s)[REP]) {
 #pragma unroll
             for (int r = 0; r < REP; ++r) {
-                kw[r] = vw[r] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-                ks[r] = vs[r] = __float2half_rn(0.0f);
-                if (page[r] >= 0) {
+                w[r] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+                s[r] = __float2half_rn(0.0f);
+                if (pg[r] >= 0) {
                     const int place = (j * CH_KEYS + tk + r * TOK) & ((1 << a.P.page_shift) - 1);
-                    const int64_t row = ((static_cast<int64_t>(page[r]) * a.P.heads + h) << a.P.page_shift) + place;
-                    kw[r] = __ldg(reinterpret_cast<const uint4*>(a.P.k + row * (D / 2)) + piece);
-                    vw[r] = __ldg(reinterpret_cast<const uint4*>(a.P.v + row * (D / 2)) + piece);
-                    ks[r] = a.P.ks[row * gpr + grp];
-                    vs[r] = a.P.vs[row * gpr + grp];
+                    const int64_t row = ((static_cast<int64_t>(pg[r]) * a.P.heads + h) << a.P.page_shift) + place;
+                    w[r] = __ldg(reinterpret_cast<const uint4*>(codes + row * (D / 2)) + piece);
+                    s[r] = scales[row * gpr + grp];
                 }
             }
         };
@@ -382,8 +381,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
             fence_proxy_async();
             __syncwarp();
         };
-        pages(j0);
-        if (j0 < j1) load(j0);
+        pages(j0, page);
+        load(j0, a.P.k, a.P.ks, page, kw, ks);
+        load(j0, a.P.v, a.P.vs, page, vw, vs);
+        pages(j0 + 1, next);
         for (int j = j0, it = 0; j < j1; ++j, ++it) {
             const int st = it & 1, ph = (it >> 1) & 1;
             uint32_t bad = 0;  // 16-token pieces with a token whose page is out of range
@@ -395,11 +396,14 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
             if (lane == 0) pbad[(j & 3) * 4 + warp - 8] = bad;
             put(sk + st * TILE, kw, ks);
             if (lane == 0) mbar_arrive(&kfull[st]);
+            load(j + 1, a.P.k, a.P.ks, next, kw, ks);
             if (!warp_wait(&vempty[st], ph ^ 1, timeout_ns, abort_flag)) break;
             put(sv + st * TILE, vw, vs);
             if (lane == 0) mbar_arrive(&vfull[st]);
-            pages(j + 1);
-            if (j + 1 < j1) load(j + 1);
+            load(j + 1, a.P.v, a.P.vs, next, vw, vs);
+#pragma unroll
+            for (int r = 0; r < REP; ++r) page[r] = next[r];
+            pages(j + 2, next);
         }
     } else {
         // ---------------------------------------------------------------- MMAs

@@ -17,19 +17,19 @@
 // real number: a key that lands on the other side of a border would change a
 // 4-bit code by a whole step, so the fused append has to round as any other
 // exact evaluation does.  The fp32 evaluation is within
-//   E = 2^-20 r (|a| + |b|)
-// of the real value: c and s within 2^-22 (the angle is reduced in fp64 and
-// rounded to fp32 turns, 2 pi 2^-26, then sincospif's two units), r within
-// 8 * 2^-24 (at most 11 additions of one-signed terms, halved by the root,
-// and the roundings of mean, sum and root), x w exact (8 + 8 bits), and three
-// more roundings.  Where a bf16 midpoint lies within E (about one value in a
-// thousand) that value is evaluated again in fp64 and rounded from there.
+//   E = 9 * 2^-24 r (|a| + |b|)
+// of the real value: c and s are fp64 values rounded once (2^-25 each), r is
+// within 5 * 2^-24 (squares exact, at most 7 additions of one-signed terms,
+// halved by the root; then the roundings of mean + eps and of the root), x w
+// is exact (8 + 8 bits), and there are three more roundings.  Where a bf16
+// midpoint lies within E (about one value in two thousand) that value is
+// evaluated again in fp64 and rounded from there.
 //
 // Bound: HBM.  A row is read and written once; 16 (D = 128) or 8 (D = 64)
 // lanes hold it, 8 adjacent values each (one 16-byte load), so the norm is a
-// shuffle reduction and the half-split partner one shuffle.  The angles of a
-// token are reduced once per CTA, which then walks the token's heads with
-// cos and sin in registers.
+// shuffle reduction and the half-split partner one shuffle.  A CTA works out
+// its token's angles once, in fp64, while the first rows are on their way, and
+// walks the token's heads with cos and sin in registers.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -119,8 +119,12 @@ __device__ __noinline__ uint32_t bf16_from_f64(double y) {
     return bf16_rn_bits(f);
 }
 
-// The token's turns (angle / 2 pi, reduced to [-1/2, 1/2]) for each pair.
-__device__ __forceinline__ void token_turns(const RopeArgs& a, int64_t token, double* turns) {
+// cos and sin of the token's angles for each pair, fp64 and rounded to fp32.
+struct TokenTurns {
+    float2 f[ROPE_MAX_PAIRS];
+    double2 d[ROPE_MAX_PAIRS];
+};
+__device__ __forceinline__ void token_turns(const RopeArgs& a, int64_t token, TokenTurns& T) {
     for (int i = threadIdx.x; i < a.pairs; i += blockDim.x) {
         int ax = 0;
 #pragma unroll
@@ -131,7 +135,10 @@ __device__ __forceinline__ void token_turns(const RopeArgs& a, int64_t token, do
         const double angle = static_cast<double>(a.pos[token * a.axes + ax]) * static_cast<double>(a.inv_freq[i]);
         const double t = angle * 0.15915494309189535;
         const double rest = fma(angle, -9.839338337591243e-18, fma(angle, 0.15915494309189535, -t));
-        turns[i] = (t - rint(t)) + rest;
+        double c, s;
+        sincospi(2.0 * ((t - rint(t)) + rest), &s, &c);
+        T.d[i] = make_double2(c, s);
+        T.f[i] = make_float2(static_cast<float>(c), static_cast<float>(s));
     }
 }
 
@@ -139,31 +146,30 @@ __device__ __forceinline__ void token_turns(const RopeArgs& a, int64_t token, do
 template <int D, bool INTER>
 struct RopeLane {
     float c[INTER ? 4 : 8], s[INTER ? 4 : 8];
-    int src;  // half-split: the lane with the partners
-    __device__ __forceinline__ void load(const RopeArgs& a, const double* turns, int lane) {
-        constexpr int LPR = D / 8;
-        const int l = lane & (LPR - 1), base = lane & ~(LPR - 1);
+    int src;    // half-split: the lane with the partners
+    int first;  // the lane's first pair, or -1: not rotated
+    bool lo;    // half-split: this lane has the pairs' first inputs
+    __device__ __forceinline__ void load(const RopeArgs& a, const TokenTurns& T, bool rope, int lane) {
+        constexpr int LPR = D / 8, NP = INTER ? 4 : 8;
+        const int l = lane & (LPR - 1), base = lane & ~(LPR - 1), h8 = a.pairs >> 3;
         if constexpr (INTER) {
             src = lane;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                c[i] = 1.0f;
-                s[i] = 0.0f;
-                if (4 * l + i < a.pairs) sincospif(static_cast<float>(2.0 * turns[4 * l + i]), &s[i], &c[i]);
-            }
+            lo = false;
+            first = rope && 4 * l < a.pairs ? 4 * l : -1;  // pairs is a multiple of 8
         } else {
-            const int h8 = a.pairs >> 3;
-            const bool lo = l < h8, rot = l < 2 * h8;
-            src = base + (lo ? l + h8 : (rot ? l - h8 : l));
-            const int p0 = 8 * (lo ? l : l - h8);
+            lo = l < h8;
+            const bool rot = rope && l < 2 * h8;
+            src = base + (!rot ? l : lo ? l + h8 : l - h8);
+            first = rot ? 8 * (lo ? l : l - h8) : -1;
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                c[i] = 1.0f;
-                s[i] = 0.0f;
-                if (rot) {
-                    sincospif(static_cast<float>(2.0 * turns[p0 + i]), &s[i], &c[i]);
-                    if (lo) s[i] = -s[i];  // the first of the pair: a c - b s
-                }
+        for (int i = 0; i < NP; ++i) {
+            c[i] = 1.0f;
+            s[i] = 0.0f;
+            if (first >= 0) {
+                const float2 v = T.f[first + i];
+                c[i] = v.x;
+                s[i] = lo ? -v.y : v.y;  // the first of the pair: a c - b s
             }
         }
     }
@@ -172,40 +178,35 @@ struct RopeLane {
 // One row: x (8 bf16 values a lane) to the rounded bits, two per word.
 template <int D, bool INTER>
 __device__ __forceinline__ uint4 norm_rope_row(uint4 raw, const float (&w)[8], bool norm, bool rope, const RopeArgs& a,
-                                               const RopeLane<D, INTER>& R, const double* turns, int lane) {
+                                               const RopeLane<D, INTER>& R, const TokenTurns& T) {
     constexpr int LPR = D / 8;
     if (!norm && !rope) return raw;
     float x[8];
     unpack8(raw, x);
     float r = 1.0f;
     if (norm) {
-        float ss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+        const float s01 = __fadd_rn(x[0] * x[0], x[1] * x[1]), s23 = __fadd_rn(x[2] * x[2], x[3] * x[3]);
+        const float s45 = __fadd_rn(x[4] * x[4], x[5] * x[5]), s67 = __fadd_rn(x[6] * x[6], x[7] * x[7]);
+        float ss = (s01 + s23) + (s45 + s67);
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         r = __frsqrt_rn(fmaf(ss, 1.0f / D, static_cast<float>(a.eps)));
     }
-    float xw[8], p[8], y[8];
-    uint32_t near = 0;  // values whose rounding the fp32 evaluation does not decide
+    float p[8], y[8], gap = INFINITY;  // the least distance of a bf16 midpoint beyond E
+    const float k = r * 5.364418029785156e-7f;  // 9 * 2^-24 r
 #pragma unroll
-    for (int i = 0; i < 8; ++i) xw[i] = x[i] * w[i];  // exact: 8 x 8 bits
+    for (int i = 0; i < 8; ++i) x[i] *= w[i];  // exact: 8 x 8 bits
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float c = 1.0f, s = 0.0f;
-        if constexpr (INTER) {
-            p[i] = xw[i ^ 1];
-            c = R.c[i / 2];
-            s = (i & 1) ? R.s[i / 2] : -R.s[i / 2];
-        } else {
-            p[i] = __shfl_sync(0xffffffffu, xw[i], R.src);
-            c = R.c[i];
-            s = R.s[i];
-        }
-        y[i] = fmaf(xw[i], c, p[i] * s) * r;
+        if constexpr (INTER) p[i] = (i & 1) ? x[i - 1] : -x[i + 1];
+        else p[i] = __shfl_sync(0xffffffffu, x[i], R.src);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float c = INTER ? R.c[i / 2] : R.c[i % (INTER ? 4 : 8)], s = INTER ? R.s[i / 2] : R.s[i % (INTER ? 4 : 8)];
+        y[i] = fmaf(x[i], c, p[i] * s) * r;
         const float mid = __uint_as_float((__float_as_uint(y[i]) & 0xFFFF0000u) | 0x8000u);
-        const float e = (fabsf(xw[i]) + fabsf(p[i])) * (r * 9.5367431640625e-7f);  // E above
-        if (fabsf(y[i] - mid) <= e) near |= 1u << i;
+        gap = fminf(gap, fmaf(fabsf(x[i]) + fabsf(p[i]), -k, fabsf(y[i] - mid)));
     }
     uint4 out;
     uint32_t* o = reinterpret_cast<uint32_t*>(&out);
@@ -214,36 +215,34 @@ __device__ __forceinline__ uint4 norm_rope_row(uint4 raw, const float (&w)[8], b
         const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
         o[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    if (__any_sync(0xffffffffu, near != 0)) {
+    if (__any_sync(0xffffffffu, gap <= 0.0f)) {
         double r64 = 1.0;
         if (norm) {
             double ss = 0.0;
+            float f[8];
+            unpack8(raw, f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), ss);
+            for (int i = 0; i < 8; ++i) ss = fma(static_cast<double>(f[i]), static_cast<double>(f[i]), ss);
 #pragma unroll
-            for (int k = LPR / 2; k > 0; k >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
+            for (int j = LPR / 2; j > 0; j >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, j);
             r64 = 1.0 / sqrt(ss / D + a.eps);
         }
-        const int l = lane & (LPR - 1);
+        if (gap <= 0.0f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (!(near >> i & 1u)) continue;
-            double c = 1.0, s = 0.0;
-            int pair = -1;
-            bool first = false;
-            if constexpr (INTER) {
-                if (4 * l + i / 2 < a.pairs) pair = 4 * l + i / 2;
-                first = (i & 1) == 0;
-            } else {
-                const int h8 = a.pairs >> 3;
-                first = l < h8;
-                if (l < 2 * h8) pair = 8 * (first ? l : l - h8) + i;
+            for (int i = 0; i < 8; ++i) {
+                const float mid = __uint_as_float((__float_as_uint(y[i]) & 0xFFFF0000u) | 0x8000u);
+                if (fmaf(fabsf(x[i]) + fabsf(p[i]), -k, fabsf(y[i] - mid)) > 0.0f) continue;
+                double c = 1.0, s = 0.0;
+                if (R.first >= 0) {
+                    const double2 t = T.d[R.first + (INTER ? i / 2 : i)];
+                    c = t.x;
+                    s = R.lo ? -t.y : t.y;
+                }
+                const uint32_t b = bf16_from_f64((static_cast<double>(x[i]) * c + static_cast<double>(p[i]) * s) * r64);
+                o[i / 2] = (i & 1) ? ((o[i / 2] & 0xFFFFu) | (b << 16)) : ((o[i / 2] & 0xFFFF0000u) | b);
             }
-            if (rope && pair >= 0) sincospi(2.0 * turns[pair], &s, &c);
-            if (first) s = -s;
-            const uint32_t b = bf16_from_f64((static_cast<double>(xw[i]) * c + static_cast<double>(p[i]) * s) * r64);
-            o[i / 2] = (i & 1) ? ((o[i / 2] & 0xFFFFu) | (b << 16)) : ((o[i / 2] & 0xFFFF0000u) | b);
         }
+        __syncwarp();
     }
     return out;
 }
@@ -251,7 +250,7 @@ __device__ __forceinline__ uint4 norm_rope_row(uint4 raw, const float (&w)[8], b
 __device__ __forceinline__ void load_weight8(const uint16_t* w, int l, float (&f)[8]) {
     if (w) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(static_cast<uint32_t>(w[8 * l + i]) << 16);
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(static_cast<uint32_t>(__ldg(w + 8 * l + i)) << 16);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = 1.0f;
@@ -264,20 +263,30 @@ template <int D, bool INTER>
 __global__ void __launch_bounds__(KV_THREADS) qk_norm_rope_kernel(const HeadRows q, const HeadRows k, const RopeArgs a,
                                                                   int64_t tokens) {
     constexpr int LPR = D / 8, RPW = 32 / LPR;
-    __shared__ double turns[ROPE_MAX_PAIRS];
+    __shared__ TokenTurns turns;
     grid_dependency_sync();
     const int64_t token = blockIdx.x;
     const bool rope = a.pos != nullptr;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (LPR - 1), sub = lane / LPR;
+    const int step = gridDim.y * (KV_THREADS / 32);
+    const int bites_q = (q.heads + RPW - 1) / RPW, bites = bites_q + (k.heads + RPW - 1) / RPW;
+    auto fetch = [&](int b) {
+        const bool isq = b < bites_q;
+        const HeadRows& S = isq ? q : k;
+        const int h = (isq ? b : b - bites_q) * RPW + sub;
+        return b < bites && h < S.heads ? *reinterpret_cast<const uint4*>(S.x + token * S.stride + static_cast<int64_t>(h) * D + 8 * l)
+                                        : make_uint4(0u, 0u, 0u, 0u);
+    };
+    int b = blockIdx.y * (KV_THREADS / 32) + warp;
+    uint4 raw = fetch(b);
     if (rope) token_turns(a, token, turns);
     __syncthreads();
     RopeLane<D, INTER> R;
-    R.load(a, turns, lane);
-    const int step = gridDim.y * (KV_THREADS / 32);
-    const int bites_q = (q.heads + RPW - 1) / RPW, bites = bites_q + (k.heads + RPW - 1) / RPW;
+    R.load(a, turns, rope, lane);
     float w[8];
     int held = -1;  // whose weight w holds
-    for (int b = blockIdx.y * (KV_THREADS / 32) + warp; b < bites; b += step) {
+    for (; b < bites; b += step) {
+        const uint4 next = fetch(b + step);
         const bool isq = b < bites_q;
         const HeadRows& S = isq ? q : k;
         if (held != static_cast<int>(isq)) {
@@ -285,11 +294,9 @@ __global__ void __launch_bounds__(KV_THREADS) qk_norm_rope_kernel(const HeadRows
             held = static_cast<int>(isq);
         }
         const int h = (isq ? b : b - bites_q) * RPW + sub;
-        const bool in = h < S.heads;
-        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-        if (in) raw = *reinterpret_cast<const uint4*>(S.x + token * S.stride + static_cast<int64_t>(h) * D + 8 * l);
-        const uint4 o = norm_rope_row<D, INTER>(raw, w, S.w != nullptr, rope, a, R, turns, lane);
-        if (in) *reinterpret_cast<uint4*>(S.out + token * S.out_stride + static_cast<int64_t>(h) * D + 8 * l) = o;
+        const uint4 o = norm_rope_row<D, INTER>(raw, w, S.w != nullptr, rope, a, R, turns);
+        if (h < S.heads) *reinterpret_cast<uint4*>(S.out + token * S.out_stride + static_cast<int64_t>(h) * D + 8 * l) = o;
+        raw = next;
     }
 }
 
@@ -333,31 +340,39 @@ template <int D, bool INTER>
 __global__ void __launch_bounds__(KV_THREADS) kv4_append_kernel(const HeadRows k, const HeadRows v, const RopeArgs a,
                                                                 const KvBatch B, const Kv4Pool P) {
     constexpr int LPR = D / 8, RPW = 32 / LPR;
-    __shared__ double turns[ROPE_MAX_PAIRS];
+    __shared__ TokenTurns turns;
     grid_dependency_sync();
     const int b = blockIdx.x / B.max_q, i = blockIdx.x - b * B.max_q;
     KvSlot slot;
     if (!kv_slot(B, P, b, i, slot)) return;  // the same for the whole CTA
     const bool rope = a.pos != nullptr;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (LPR - 1), sub = lane / LPR;
-    if (rope) token_turns(a, slot.row, turns);
-    __syncthreads();
-    RopeLane<D, INTER> R;
-    R.load(a, turns, lane);
-    float w[8];
-    load_weight8(k.w, l, w);
     const int step = gridDim.y * (KV_THREADS / 32);
     const int bites_k = (P.heads + RPW - 1) / RPW;
+    auto fetch = [&](int t) {
+        const bool isk = t < bites_k;
+        const HeadRows& S = isk ? k : v;
+        const int h = (isk ? t : t - bites_k) * RPW + sub;
+        return t < 2 * bites_k && h < P.heads ? *reinterpret_cast<const uint4*>(S.x + slot.row * S.stride + static_cast<int64_t>(h) * D + 8 * l)
+                                              : make_uint4(0u, 0u, 0u, 0u);
+    };
+    int t = blockIdx.y * (KV_THREADS / 32) + warp;
+    uint4 next = fetch(t);
+    if (rope) token_turns(a, slot.row, turns);
+    float w[8];
+    load_weight8(k.w, l, w);
+    __syncthreads();
+    RopeLane<D, INTER> R;
+    R.load(a, turns, rope, lane);
     const int lg8 = P.lg_group - 3;  // log2 of the lanes of a group
     bool bad = false;
-    for (int t = blockIdx.y * (KV_THREADS / 32) + warp; t < 2 * bites_k; t += step) {
+    for (; t < 2 * bites_k; t += step) {
+        uint4 raw = next;
+        next = fetch(t + step);
         const bool isk = t < bites_k;
         const int h = (isk ? t : t - bites_k) * RPW + sub;
         const bool in = h < P.heads;
-        const HeadRows& S = isk ? k : v;
-        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-        if (in) raw = *reinterpret_cast<const uint4*>(S.x + slot.row * S.stride + static_cast<int64_t>(h) * D + 8 * l);
-        if (isk) raw = norm_rope_row<D, INTER>(raw, w, k.w != nullptr, rope, a, R, turns, lane);
+        if (isk) raw = norm_rope_row<D, INTER>(raw, w, k.w != nullptr, rope, a, R, turns);
         uint32_t m2 = __vmaxu2(__vmaxu2(raw.x & 0x7FFF7FFFu, raw.y & 0x7FFF7FFFu),
                                __vmaxu2(raw.z & 0x7FFF7FFFu, raw.w & 0x7FFF7FFFu));
         uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
