@@ -39,11 +39,12 @@ namespace wlq {
 
 constexpr int CH_ROWS = 128;  // rows of a tile
 constexpr int CH_KEYS = 128;  // cached tokens of a step
-constexpr int CH_THREADS = 512;  // two softmax warpgroups, one of dequantisation, one whose first warp issues MMAs
+// Two softmax warpgroups, one that dequantises keys, one values, one whose first warp issues MMAs.
+constexpr int CH_THREADS = 640;
 constexpr int CH_STAGES = 2;
-// Registers a thread of each role, moved after the start: 2 x 176 + 112 + 48 = 4 x 128, what the block was launched with.
-constexpr int CH_REGS_SOFTMAX = 176, CH_REGS_DEQUANT = 112, CH_REGS_MMA = 48;
-static_assert(2 * CH_REGS_SOFTMAX + CH_REGS_DEQUANT + CH_REGS_MMA == 4 * 128, "register shares");
+// Registers a thread of each role, moved after the start: 2 x 152 + 2 x 72 + 32 = 5 x 96, what the block was launched with.
+constexpr int CH_REGS_SOFTMAX = 152, CH_REGS_DEQUANT = 72, CH_REGS_MMA = 32;
+static_assert(2 * CH_REGS_SOFTMAX + 2 * CH_REGS_DEQUANT + CH_REGS_MMA == 5 * 96, "register shares");
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -54,17 +55,34 @@ __host__ __device__ constexpr uint32_t ch_tile_bytes() { return 128u * D * 2u; }
 template <int D>
 __host__ __device__ constexpr size_t ch_smem_bytes() { return 1024 + (2 + 2 * CH_STAGES) * ch_tile_bytes<D>() + 256; }
 
-// Shared-memory descriptor of an MN-major operand with the 128-byte swizzle:
-// rows of 64 MN values (128 bytes), eight of them (1024 bytes) a swizzle atom,
-// the next 64 MN values `chunk` bytes away.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t chunk) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(chunk >> 4) << 16;  // leading byte offset: the next 64 MN values
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;   // stride byte offset: the next 8 rows of K
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
+// Low words of shared-memory descriptors (128-byte swizzle, version 1); the
+// high word is the same for all of them: eight rows are 1024 bytes apart.
+// K-major: the leading offset is unused.  MN-major: rows of 64 MN values (128
+// bytes), the next 64 MN values `chunk` bytes away (leading offset).
+constexpr uint32_t CH_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo_k(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr, uint32_t chunk) { return ((saddr & 0x3FFFFu) >> 4) | ((chunk >> 4) << 16); }
+
+// mma_ss / mma_ts with descriptors given by their low words: the issuing thread
+// has few registers, and 64-bit descriptors held across the steps would spill.
+__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %5};\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(CH_DESC_HI)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(CH_DESC_HI)
+        : "memory");
 }
 
 // Cached-token steps [jb, je) of a row tile within the CTA's split.
@@ -152,7 +170,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 12) tmem_alloc(tmem_slot, 512);
+    if (warp == 16) tmem_alloc(tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -322,110 +340,108 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
             }
             tc_fence_before();
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ----------------------------------------------------- dequantisation
         regs_dec<CH_REGS_DEQUANT>();
-        constexpr int CPT = D / 32;           // 16-byte pieces of a token's codes
-        constexpr int TOK = 128 / CPT;        // tokens the 128 threads take at once
-        constexpr int REP = 128 / TOK;        // pieces a thread has of a tile
-        const int i = threadIdx.x - 256, piece = i % CPT, tk = i / CPT;
+        const bool isv = warp >= 12;
+        constexpr int CPT = D / 32;     // 16-byte pieces of a token's codes
+        constexpr int TOK = 128 / CPT;  // tokens the 128 threads take at once
+        constexpr int REP = 128 / TOK;  // pieces a thread has of a tile
+        const int i = threadIdx.x & 127, piece = i % CPT, tk = i / CPT;
         const int lg = a.P.lg_group, gpr = D >> lg, grp = (piece * 32) >> lg;
-        int page[REP], next[REP];  // this step's pages (-1: none or out of range), the next one's
-        uint4 kw[REP], vw[REP];
-        __half ks[REP], vs[REP];
-        auto pages = [&](int j, int (&pg)[REP]) {
+        const int shift = a.P.page_shift, pmask = (1 << shift) - 1;
+        const uint4* codes = reinterpret_cast<const uint4*>(isv ? a.P.v : a.P.k) + piece;
+        const __half* scales = (isv ? a.P.vs : a.P.ks) + grp;
+        const int32_t* table = a.B.table + b * a.B.table_stride;
+        uint8_t* tiles = isv ? sv : sk;
+        uint64_t* full = isv ? vfull : kfull;
+        uint64_t* empty = isv ? vempty : kempty;
+        int32_t page[REP];  // of the step that is loaded next, as the table has them (-1: none)
+        uint4 w[REP];
+        __half sc[REP];
+        uint32_t bad = 0;  // 16-token pieces with a token whose page is out of range
+        auto pages = [&](int j) {
 #pragma unroll
             for (int r = 0; r < REP; ++r) {
                 const int tok = j * CH_KEYS + tk + r * TOK;
-                pg[r] = -1;
-                if (j < j1 && tok < kv) {
-                    const int64_t e = tok >> a.P.page_shift;
-                    if (e < a.B.table_stride) pg[r] = a.B.table[b * a.B.table_stride + e];
-                    if (!kv_page_ok(pg[r], a.P.pages)) {
-                        raise_error(ERRBIT_INDEX);
-                        pg[r] = -1;
-                    }
-                }
+                page[r] = -1;
+                if (j < j1 && tok < kv && (tok >> shift) < a.B.table_stride) page[r] = __ldg(table + (tok >> shift));
             }
         };
         // codes and scales of step j (zeros where there is no token)
-        auto load = [&](int j, const uint8_t* codes, const __half* scales, const int (&pg)[REP], uint4 (&w)[REP], __half (&s)[REP]) {
+        auto load = [&](int j) {
+            bad = 0;
 #pragma unroll
             for (int r = 0; r < REP; ++r) {
+                const int tok = j * CH_KEYS + tk + r * TOK;
+                const bool is = j < j1 && tok < kv, in = is && kv_page_ok(page[r], a.P.pages);
+                if (is && !in) bad |= 1u << ((tk + r * TOK) >> 4);
                 w[r] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-                s[r] = __float2half_rn(0.0f);
-                if (pg[r] >= 0) {
-                    const int place = (j * CH_KEYS + tk + r * TOK) & ((1 << a.P.page_shift) - 1);
-                    const int64_t row = ((static_cast<int64_t>(pg[r]) * a.P.heads + h) << a.P.page_shift) + place;
-                    w[r] = __ldg(reinterpret_cast<const uint4*>(codes + row * (D / 2)) + piece);
-                    s[r] = scales[row * gpr + grp];
+                sc[r] = __float2half_rn(0.0f);
+                if (in) {
+                    const int64_t row = ((static_cast<int64_t>(page[r]) * a.P.heads + h) << shift) + (tok & pmask);
+                    w[r] = __ldg(codes + row * CPT);
+                    sc[r] = __ldg(scales + row * gpr);
                 }
             }
         };
-        auto put = [&](uint8_t* tile, const uint4 (&w)[REP], const __half (&s)[REP]) {
+        pages(j0);
+        load(j0);
+        pages(j0 + 1);
+        for (int j = j0, it = 0; j < j1; ++j, ++it) {
+            const int st = it & 1, ph = (it >> 1) & 1;
+            if (!warp_wait(&empty[st], ph ^ 1, timeout_ns, abort_flag)) break;
+            uint8_t* tile = tiles + st * TILE + (piece / 2) * HALF;
 #pragma unroll
             for (int r = 0; r < REP; ++r) {
                 const int tok = tk + r * TOK;
                 const uint32_t x[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
-                const __half2 s2 = __half2half2(s[r]);
-                uint8_t* rowp = tile + (piece / 2) * HALF + tok * 128;
+                const __half2 s2 = __half2half2(sc[r]);
                 const bool odd = CPT == 4 && (piece & 2);  // the other column block: another store order
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t o[4];
                     nibbles_f16(odd ? x[k ^ 2] : x[k], s2, o);
                     const int unit = (piece & 1) * 4 + (odd ? (k ^ 2) : k);
-                    *reinterpret_cast<uint4*>(rowp + ((unit ^ (tok & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(tile + tok * 128 + ((unit ^ (tok & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+            if (!isv) {
+                bad = __reduce_or_sync(0xffffffffu, bad);
+                if (lane == 0) {
+                    pbad[(j & 3) * 4 + warp - 8] = bad;
+                    if (bad) raise_error(ERRBIT_INDEX);
                 }
             }
             fence_proxy_async();
             __syncwarp();
-        };
-        pages(j0, page);
-        load(j0, a.P.k, a.P.ks, page, kw, ks);
-        load(j0, a.P.v, a.P.vs, page, vw, vs);
-        pages(j0 + 1, next);
-        for (int j = j0, it = 0; j < j1; ++j, ++it) {
-            const int st = it & 1, ph = (it >> 1) & 1;
-            uint32_t bad = 0;  // 16-token pieces with a token whose page is out of range
-#pragma unroll
-            for (int r = 0; r < REP; ++r)
-                if (page[r] < 0 && j * CH_KEYS + tk + r * TOK < kv) bad |= 1u << ((tk + r * TOK) >> 4);
-            bad = __reduce_or_sync(0xffffffffu, bad);
-            if (!warp_wait(&kempty[st], ph ^ 1, timeout_ns, abort_flag)) break;
-            if (lane == 0) pbad[(j & 3) * 4 + warp - 8] = bad;
-            put(sk + st * TILE, kw, ks);
-            if (lane == 0) mbar_arrive(&kfull[st]);
-            load(j + 1, a.P.k, a.P.ks, next, kw, ks);
-            if (!warp_wait(&vempty[st], ph ^ 1, timeout_ns, abort_flag)) break;
-            put(sv + st * TILE, vw, vs);
-            if (lane == 0) mbar_arrive(&vfull[st]);
-            load(j + 1, a.P.v, a.P.vs, next, vw, vs);
-#pragma unroll
-            for (int r = 0; r < REP; ++r) page[r] = next[r];
-            pages(j + 2, next);
+            if (lane == 0) mbar_arrive(&full[st]);
+            load(j + 1);
+            pages(j + 2);
         }
     } else {
         // ---------------------------------------------------------------- MMAs
         regs_dec<CH_REGS_MMA>();
-        if (warp == 12 && lane == 0) {
+        if (warp == 16 && lane == 0) {
         constexpr uint32_t id_s = idesc_f16(0, 128, CH_KEYS);
         constexpr uint32_t id_o = idesc_f16(0, 128, D) | (1u << 16);  // B is MN-major
         int cnt[2] = {0, 0};  // weight steps of each tile so far
         bool ok = nv_wait(qfull, 0, timeout_ns, abort_flag);
-        auto scores = [&](int t, int j, int it) {  // S_t = Q_t K_j^T
-            const uint32_t qa = smem_u32(sq + t * TILE), ka = smem_u32(sk + (it & 1) * TILE);
+        const uint32_t q_lo = desc_lo_k(smem_u32(sq)), k_lo = desc_lo_k(smem_u32(sk)), v_lo = desc_lo_mn(smem_u32(sv), HALF);
+        auto scores = [&](int t, int it) {  // S_t = Q_t K^T
+            uint32_t qa = q_lo + t * (TILE >> 4), ka = k_lo + (it & 1) * (TILE >> 4);
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c, qa += HALF >> 4, ka += HALF >> 4)
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                mma_ss(tmem + t * 128, smem_desc_sw128(qa + (k / 4) * HALF) + 2 * (k % 4), smem_desc_sw128(ka + (k / 4) * HALF) + 2 * (k % 4),
-                       id_s, k > 0 ? 1u : 0u);
+                for (int k = 0; k < 4; ++k) mma_ss_lo(tmem + t * 128, qa + 2 * k, ka + 2 * k, id_s, c + k);
             mma_commit(&sfull[t]);
         };
-        auto outputs = [&](int t, int j, int it) {  // O_t += P_t V_j
-            const uint64_t vd = smem_desc_mn_sw128(smem_u32(sv + (it & 1) * TILE), HALF);
+        auto outputs = [&](int t, int it) {  // O_t += P_t V
+            uint32_t va = v_lo + (it & 1) * (TILE >> 4), pa = tmem + t * 128;
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c, va += 4 * 128, pa += 4 * 8)
 #pragma unroll
-            for (int k = 0; k < CH_KEYS / 16; ++k)
-                mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * k, vd + static_cast<uint64_t>(k * 2048 / 16), id_o, (cnt[t] > 0 || k > 0) ? 1u : 0u);
+                for (int k = 0; k < 4; ++k) mma_ts_lo(tmem + 256 + t * 128, pa + 8 * k, va + 128 * k, id_o, cnt[t] + c + k);
             mma_commit(&pvdone[t]);
             ++cnt[t];
         };
@@ -434,7 +450,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
             if (ok) {
                 tc_fence_after();
                 for (int t = 0; t < 2; ++t)
-                    if (R[t].at(j0)) scores(t, j0, 0);
+                    if (R[t].at(j0)) scores(t, 0);
                 mma_commit(&kempty[0]);
             }
         }
@@ -447,7 +463,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
                 if (R[t].at(j)) {
                     if (!(ok = nv_wait(&pfull[t], cnt[t] & 1, timeout_ns, abort_flag))) break;
                     tc_fence_after();
-                    outputs(t, j, it);
+                    outputs(t, it);
                 }
                 if (t == 1) mma_commit(&vempty[st]);
                 if (more) {
@@ -456,7 +472,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
                         tc_fence_after();
                         knext = true;
                     }
-                    if (R[t].at(j + 1)) scores(t, j + 1, it + 1);
+                    if (R[t].at(j + 1)) scores(t, it + 1);
                     if (t == 1) mma_commit(&kempty[st ^ 1]);
                 }
             }
@@ -470,7 +486,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
         __syncwarp();
     }
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 16) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
