@@ -5,10 +5,11 @@
 // two tiles of 128 and walks the cached tokens in tiles of 128:
 //   S_t = Q_t K^T   (shared memory x shared memory, fp32 in tensor memory)
 //   P_t = exp2(S_t c - m)   as fp16 over S_t's own tensor-memory columns
-//   O_t += P_t V    (tensor memory x shared memory)
+//   O_t += P_t V    (tensor memory x shared memory), in two halves of 64 tokens
 // Roles: two warpgroups of softmax (a thread owns a row: no shuffles), one of
 // dequantisation, one warp that issues MMAs.  While one tile's weights are
-// computed the tensor cores work on the other: the issue order is PV_0(j),
+// computed the tensor cores work on the other, and on the first half of these
+// weights while the second is computed: the issue order is PV_0(j),
 // QK_0(j+1), PV_1(j), QK_1(j+1), and since they execute in that order S_t(j+1)
 // may overwrite the columns PV_t(j) has read.
 //
@@ -42,8 +43,8 @@ constexpr int CH_KEYS = 128;  // cached tokens of a step
 // Two softmax warpgroups, one that dequantises keys, one values, one whose first warp issues MMAs.
 constexpr int CH_THREADS = 640;
 constexpr int CH_STAGES = 2;
-// Registers a thread of each role, moved after the start: 2 x 152 + 2 x 72 + 32 = 5 x 96, what the block was launched with.
-constexpr int CH_REGS_SOFTMAX = 152, CH_REGS_DEQUANT = 72, CH_REGS_MMA = 32;
+// Registers a thread of each role, moved after the start: 2 x 128 + 2 x 80 + 64 = 5 x 96, what the block was launched with.
+constexpr int CH_REGS_SOFTMAX = 128, CH_REGS_DEQUANT = 80, CH_REGS_MMA = 64;
 static_assert(2 * CH_REGS_SOFTMAX + 2 * CH_REGS_DEQUANT + CH_REGS_MMA == 5 * 96, "register shares");
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -63,25 +64,46 @@ constexpr uint32_t CH_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo_k(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
 __device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr, uint32_t chunk) { return ((saddr & 0x3FFFFu) >> 4) | ((chunk >> 4) << 16); }
 
-// mma_ss / mma_ts with descriptors given by their low words: the issuing thread
-// has few registers, and 64-bit descriptors held across the steps would spill.
-__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+// mma_ss / mma_ts / mma_commit issued by a whole converged warp, executed by its
+// lane with `on` set: addresses and descriptors (given by their low words) then
+// stay uniform values, which the instruction wants; from a divergent branch
+// every operand is moved there one by one, about twice the MMA's own 64 clocks.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t on;
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(on));
+    return on;
+}
+__device__ __forceinline__ void mma_ss_lo(uint32_t on, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
         "mov.b64 a, {%1, %5};\n\t"
         "mov.b64 b, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(CH_DESC_HI)
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(CH_DESC_HI), "r"(on)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts_lo(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
         "mov.b64 b, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(CH_DESC_HI)
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(CH_DESC_HI), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit_on(uint32_t on, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(on)
         : "memory");
 }
 
@@ -106,11 +128,12 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
     uint64_t* vfull = bars + 4;              // [2]
     uint64_t* vempty = bars + 6;             // [2]
     uint64_t* sfull = bars + 8;              // [2] scores of tile t are in tensor memory
-    uint64_t* pfull = bars + 10;             // [2] weights of tile t are
-    uint64_t* pvdone = bars + 12;            // [2] O_t has them
-    uint64_t* qfull = bars + 14;
-    uint64_t* drain = bars + 15;
-    uint32_t* pbad = reinterpret_cast<uint32_t*>(bars + 16);  // [4 steps][4 warps] a bit for each 16 tokens whose page is out of range
+    uint64_t* pfull = bars + 10;             // [2][2] a half step's weights of tile t are (a barrier for each half: the
+                                             // second may be there before the MMA warp has looked for the first)
+    uint64_t* pvdone = bars + 14;            // [2][2] O_t has a half step's weights
+    uint64_t* qfull = bars + 18;
+    uint64_t* drain = bars + 19;
+    uint32_t* pbad = reinterpret_cast<uint32_t*>(bars + 20);  // [4 steps][4 warps] a bit for each 16 tokens whose page is out of range
     uint32_t* tmem_slot = pbad + 16;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -162,8 +185,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
             mbar_init(&vfull[i], 4);
             mbar_init(&vempty[i], 1);
             mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[i], 4);
-            mbar_init(&pvdone[i], 1);
+            mbar_init(&pfull[2 * i], 4);
+            mbar_init(&pfull[2 * i + 1], 4);
+            mbar_init(&pvdone[2 * i], 1);
+            mbar_init(&pvdone[2 * i + 1], 1);
         }
         mbar_init(qfull, 8);
         mbar_init(drain, 1);
@@ -237,72 +262,77 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
             const uint4 bad4 = *reinterpret_cast<const uint4*>(pbad + (j & 3) * 4);
             const uint32_t bad = bad4.x | bad4.y | bad4.z | bad4.w;
             const bool inside = __all_sync(0xffffffffu, k0 >= lo && k0 + CH_KEYS <= hi && bad == 0);
-            uint32_t v[8][16];
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch) tmem_ld16(s_t + 16 * ch, v[ch]);
-            tmem_wait_ld();
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch) reg_pin(v[ch]);
-            if (!inside) {
-#pragma unroll
-                for (int ch = 0; ch < 8; ++ch) {
-                    // keys of this piece from `first` to `last` are seen
-                    const int first = lo - k0 - 16 * ch, last = (bad >> ch & 1u) ? 0 : hi - k0 - 16 * ch;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (i < first || i >= last) v[ch][i] = 0xFF800000u;
-                }
-            }
-            float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch)
-#pragma unroll
-                for (int i = 0; i < 16; i += 2)
-                    top4[(i / 2) & 3] = fmaxf(top4[(i / 2) & 3], fmaxf(__uint_as_float(v[ch][i]), __uint_as_float(v[ch][i + 1])));
-            const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * c;  // c > 0
-            const bool move = top > m + ATT_LAZY;  // also from -inf
-            if (__any_sync(0xffffffffu, move)) {
-                const float f = move ? ex2(m - top) : 1.0f;  // 0 from -inf
-                if (move) m = top;
-                l *= f;
-                if (done > 0) {
-                    if (!warp_wait(&pvdone[t], (done - 1) & 1, timeout_ns, abort_flag)) { ok = false; break; }
-                    tc_fence_after();
 #pragma unroll 1
-                    for (int d = 0; d < D; d += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(o_t + d, o);
-                        tmem_wait_ld_pin(o);
+            for (int half = 0; half < 2; ++half) {
+                uint32_t v[4][16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st16(o_t + d, o);
+                for (int ch = 0; ch < 4; ++ch) tmem_ld16(s_t + 64 * half + 16 * ch, v[ch]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) reg_pin(v[ch]);
+                if (!inside) {
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        // keys of this piece from `first` to `last` are seen
+                        const int at = k0 + 64 * half + 16 * ch;
+                        const int first = lo - at, last = (bad >> (4 * half + ch) & 1u) ? 0 : hi - at;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (i < first || i >= last) v[ch][i] = 0xFF800000u;
                     }
-                    tmem_wait_st();
                 }
-            }
-            const float nm = m == -INFINITY ? 0.0f : -m;  // nothing seen yet: every score is -inf
-            float sum[2] = {0.0f, 0.0f};
+                float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-                uint32_t pk[16];
+                for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float p0 = ex2(fmaf(__uint_as_float(v[2 * ch + i / 8][(2 * i) & 15]), c, nm));
-                    const float p1 = ex2(fmaf(__uint_as_float(v[2 * ch + i / 8][(2 * i + 1) & 15]), c, nm));
-                    sum[0] += p0;
-                    sum[1] += p1;
-                    pk[i] = h2_bits(__floats2half2_rn(p0, p1));
+                    for (int i = 0; i < 16; i += 2)
+                        top4[(i / 2) & 3] = fmaxf(top4[(i / 2) & 3], fmaxf(__uint_as_float(v[ch][i]), __uint_as_float(v[ch][i + 1])));
+                const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * c;  // c > 0
+                const bool move = top > m + ATT_LAZY;  // also from -inf
+                if (__any_sync(0xffffffffu, move)) {
+                    const float f = move ? ex2(m - top) : 1.0f;  // 0 from -inf
+                    if (move) m = top;
+                    l *= f;
+                    if (done + half > 0) {  // O_t has what came before: the last step's second half, or this one's first
+                        if (!warp_wait(&pvdone[2 * t + (half ^ 1)], (done + half - 1) & 1, timeout_ns, abort_flag)) { ok = false; break; }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int d = 0; d < D; d += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(o_t + d, o);
+                            tmem_wait_ld_pin(o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st16(o_t + d, o);
+                        }
+                        tmem_wait_st();
+                    }
                 }
-                tmem_st16(s_t + 16 * ch, pk);
+                const float nm = m == -INFINITY ? 0.0f : -m;  // nothing seen yet: every score is -inf
+                float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float p0 = ex2(fmaf(__uint_as_float(v[2 * ch + i / 8][(2 * i) & 15]), c, nm));
+                        const float p1 = ex2(fmaf(__uint_as_float(v[2 * ch + i / 8][(2 * i + 1) & 15]), c, nm));
+                        sum[0] += p0;
+                        sum[1] += p1;
+                        pk[i] = h2_bits(__floats2half2_rn(p0, p1));
+                    }
+                    tmem_st16(s_t + 32 * half + 16 * ch, pk);  // over scores that have been read
+                }
+                l += sum[0] + sum[1];
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pfull[2 * t + half]);
             }
-            l += sum[0] + sum[1];
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&pfull[t]);
+            if (!ok) break;
         }
         // the row's result
-        if (ok && done > 0) ok = warp_wait(&pvdone[t], (done - 1) & 1, timeout_ns, abort_flag);
+        if (ok && done > 0) ok = warp_wait(&pvdone[2 * t + 1], (done - 1) & 1, timeout_ns, abort_flag);
         if (ok) {
             tc_fence_after();
             const int64_t head_row = token * a.q_heads + head;
@@ -422,66 +452,71 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
     } else {
         // ---------------------------------------------------------------- MMAs
         regs_dec<CH_REGS_MMA>();
-        if (warp == 16 && lane == 0) {
-        constexpr uint32_t id_s = idesc_f16(0, 128, CH_KEYS);
-        constexpr uint32_t id_o = idesc_f16(0, 128, D) | (1u << 16);  // B is MN-major
-        int cnt[2] = {0, 0};  // weight steps of each tile so far
-        bool ok = nv_wait(qfull, 0, timeout_ns, abort_flag);
-        const uint32_t q_lo = desc_lo_k(smem_u32(sq)), k_lo = desc_lo_k(smem_u32(sk)), v_lo = desc_lo_mn(smem_u32(sv), HALF);
-        auto scores = [&](int t, int it) {  // S_t = Q_t K^T
-            uint32_t qa = q_lo + t * (TILE >> 4), ka = k_lo + (it & 1) * (TILE >> 4);
-#pragma unroll 1
-            for (int c = 0; c < D / 64; ++c, qa += HALF >> 4, ka += HALF >> 4)
+        if (warp == 16) {
+            constexpr uint32_t id_s = idesc_f16(0, 128, CH_KEYS);
+            constexpr uint32_t id_o = idesc_f16(0, 128, D) | (1u << 16);  // B is MN-major
+            const uint32_t on = elect_one();
+            const uint32_t q_lo = desc_lo_k(smem_u32(sq)), k_lo = desc_lo_k(smem_u32(sk)), v_lo = desc_lo_mn(smem_u32(sv), HALF);
+            uint32_t cnt[2] = {0, 0};  // half steps of weights of each tile so far
+            bool ok = warp_wait(qfull, 0, timeout_ns, abort_flag);
+            auto scores = [&](int t, int it) {  // S_t = Q_t K^T
+                const uint32_t qa = q_lo + t * (TILE >> 4), ka = k_lo + (it & 1) * (TILE >> 4);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_ss_lo(tmem + t * 128, qa + 2 * k, ka + 2 * k, id_s, c + k);
-            mma_commit(&sfull[t]);
-        };
-        auto outputs = [&](int t, int it) {  // O_t += P_t V
-            uint32_t va = v_lo + (it & 1) * (TILE >> 4), pa = tmem + t * 128;
-#pragma unroll 1
-            for (int c = 0; c < 2; ++c, va += 4 * 128, pa += 4 * 8)
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k / 4) * (HALF >> 4) + 2 * (k % 4);
+                    mma_ss_lo(on, tmem + t * 128, qa + off, ka + off, id_s, k);
+                }
+                mma_commit_on(on, &sfull[t]);
+            };
+            auto outputs = [&](int t, int it, int half) {  // O_t += P_t V over 64 tokens
+                const uint32_t va = v_lo + (it & 1) * (TILE >> 4) + half * 4 * 128, pa = tmem + t * 128 + half * 32;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_ts_lo(tmem + 256 + t * 128, pa + 8 * k, va + 128 * k, id_o, cnt[t] + c + k);
-            mma_commit(&pvdone[t]);
-            ++cnt[t];
-        };
-        if (ok && j0 < j1) {
-            ok = nv_wait(&kfull[0], 0, timeout_ns, abort_flag);
-            if (ok) {
-                tc_fence_after();
-                for (int t = 0; t < 2; ++t)
-                    if (R[t].at(j0)) scores(t, 0);
-                mma_commit(&kempty[0]);
-            }
-        }
-        for (int j = j0, it = 0; ok && j < j1; ++j, ++it) {
-            const int st = it & 1;
-            if (!(ok = nv_wait(&vfull[st], (it >> 1) & 1, timeout_ns, abort_flag))) break;
-            const bool more = j + 1 < j1;
-            bool knext = false;
-            for (int t = 0; t < 2 && ok; ++t) {
-                if (R[t].at(j)) {
-                    if (!(ok = nv_wait(&pfull[t], cnt[t] & 1, timeout_ns, abort_flag))) break;
+                for (int k = 0; k < 4; ++k) mma_ts_lo(on, tmem + 256 + t * 128, pa + 8 * k, va + 128 * k, id_o, cnt[t] + k);
+                mma_commit_on(on, &pvdone[2 * t + half]);
+                ++cnt[t];
+            };
+            if (ok && j0 < j1) {
+                ok = warp_wait(&kfull[0], 0, timeout_ns, abort_flag);
+                if (ok) {
                     tc_fence_after();
-                    outputs(t, it);
-                }
-                if (t == 1) mma_commit(&vempty[st]);
-                if (more) {
-                    if (!knext) {
-                        if (!(ok = nv_wait(&kfull[st ^ 1], ((it + 1) >> 1) & 1, timeout_ns, abort_flag))) break;
-                        tc_fence_after();
-                        knext = true;
-                    }
-                    if (R[t].at(j + 1)) scores(t, it + 1);
-                    if (t == 1) mma_commit(&kempty[st ^ 1]);
+                    for (int t = 0; t < 2; ++t)
+                        if (R[t].at(j0)) scores(t, 0);
+                    mma_commit_on(on, &kempty[0]);
                 }
             }
-        }
-        // every MMA issued has completed before tensor memory is freed
-        mma_commit(drain);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < timeout_ns) {
-        }
+            for (int j = j0, it = 0; ok && j < j1; ++j, ++it) {
+                const int st = it & 1;
+                if (!(ok = warp_wait(&vfull[st], (it >> 1) & 1, timeout_ns, abort_flag))) break;
+                const bool more = j + 1 < j1;
+                bool knext = false;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (R[t].at(j)) {
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            if (!(ok = warp_wait(&pfull[2 * t + half], (cnt[t] >> 1) & 1, timeout_ns, abort_flag))) break;
+                            tc_fence_after();
+                            outputs(t, it, half);
+                        }
+                        if (!ok) break;
+                    }
+                    if (t == 1) mma_commit_on(on, &vempty[st]);
+                    if (more) {
+                        if (!knext) {
+                            if (!(ok = warp_wait(&kfull[st ^ 1], ((it + 1) >> 1) & 1, timeout_ns, abort_flag))) break;
+                            tc_fence_after();
+                            knext = true;
+                        }
+                        if (R[t].at(j + 1)) scores(t, it + 1);
+                        if (t == 1) mma_commit_on(on, &kempty[st ^ 1]);
+                    }
+                }
+            }
+            // every MMA issued has completed before tensor memory is freed
+            mma_commit_on(on, drain);
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < timeout_ns) {
+            }
         }
         __syncwarp();
     }
