@@ -43,8 +43,8 @@ constexpr int CH_KEYS = 128;  // cached tokens of a step
 // Two softmax warpgroups, one that dequantises keys, one values, one whose first warp issues MMAs.
 constexpr int CH_THREADS = 640;
 constexpr int CH_STAGES = 2;
-// Registers a thread of each role, moved after the start: 2 x 128 + 2 x 80 + 64 = 5 x 96, what the block was launched with.
-constexpr int CH_REGS_SOFTMAX = 128, CH_REGS_DEQUANT = 80, CH_REGS_MMA = 64;
+// Registers a thread of each role, moved after the start: 2 x 120 + 2 x 96 + 48 = 5 x 96, what the block was launched with.
+constexpr int CH_REGS_SOFTMAX = 120, CH_REGS_DEQUANT = 96, CH_REGS_MMA = 48;
 static_assert(2 * CH_REGS_SOFTMAX + 2 * CH_REGS_DEQUANT + CH_REGS_MMA == 5 * 96, "register shares");
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
