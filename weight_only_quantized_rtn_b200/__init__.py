@@ -109,8 +109,11 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())  # torch.cuda.current_stream(), without the object
 
 
 def groups(K: int, group: int) -> int:
@@ -335,25 +338,28 @@ def _want(ok: bool, what: str):
 
 def _on(*tensors):
     """Every tensor on the current CUDA device, where the launch goes."""
-    cur = torch.cuda.current_device()
+    cur = torch._C._cuda_getDevice()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != cur):
+        if t is not None and t.get_device() != cur:  # -1 on the host
             raise WlqError(ERR_INVALID_ARG, "tensors must be on the current CUDA device (cuda:%d)" % cur)
 
 
 def _head_rows(name: str, x, head_dim: int):
     """(pointer, token stride, heads) of bf16 x [tokens, heads, head_dim], heads contiguous within a token."""
     T, H, D = x.shape
-    st = x.stride()
-    _want(x.dtype == torch.bfloat16, name + " must be bf16")
-    _want(D == head_dim and (st[2] == 1 or D <= 1) and (st[1] == D or H <= 1), name + ": a token's heads must be contiguous")
-    return x.data_ptr(), st[0] if T > 1 else H * D, H
+    st, sh, sd = x.stride()
+    if x.dtype is not torch.bfloat16:
+        raise WlqError(ERR_INVALID_ARG, name + " must be bf16")
+    if D != head_dim or sd != 1 or (sh != D and H > 1):
+        raise WlqError(ERR_INVALID_ARG, name + ": a token's heads must be contiguous")
+    return x.data_ptr(), st if T > 1 else H * D, H
 
 
 def _weight(name: str, w, head_dim: int):
     if w is None:
         return None
-    _want(w.dtype == torch.bfloat16 and w.numel() == head_dim and w.is_contiguous(), name + " must be contiguous bf16 [head_dim]")
+    if w.dtype is not torch.bfloat16 or w.numel() != head_dim or not w.is_contiguous():
+        raise WlqError(ERR_INVALID_ARG, name + " must be contiguous bf16 [head_dim]")
     return w.data_ptr()
 
 
@@ -364,14 +370,16 @@ def _rope(positions, inv_freq, sections, tokens: int):
     """(positions, axes, inv_freq, rotary_dim, sections) for the C call."""
     if positions is None:
         return None, 0, None, 0, None
-    _want(inv_freq is not None, "positions need inv_freq")
-    _want(positions.dtype == torch.int32 and positions.is_contiguous(), "positions must be contiguous int32")
-    _want(inv_freq.dtype == torch.float32 and inv_freq.is_contiguous() and inv_freq.dim() == 1, "inv_freq must be contiguous fp32 [pairs]")
-    axes = positions.shape[1] if positions.dim() == 2 else 1
-    _want(positions.dim() in (1, 2) and positions.shape[0] == tokens, "positions must be [tokens] or [tokens, axes]")
+    if inv_freq is None or inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise WlqError(ERR_INVALID_ARG, "positions need inv_freq, contiguous fp32 [pairs]")
+    shape = positions.shape
+    axes = shape[1] if len(shape) == 2 else 1
+    if positions.dtype is not torch.int32 or not positions.is_contiguous() or len(shape) > 2 or shape[0] != tokens:
+        raise WlqError(ERR_INVALID_ARG, "positions must be contiguous int32 [tokens] or [tokens, axes]")
     pairs = inv_freq.shape[0]
     sections = (pairs,) if sections is None else tuple(sections)
-    _want(len(sections) == axes, "one section for each axis")
+    if len(sections) != axes:
+        raise WlqError(ERR_INVALID_ARG, "one section for each axis")
     arr = _SECTIONS.get(sections)
     if arr is None:
         arr = _SECTIONS[sections] = (ctypes.c_int32 * axes)(*sections)
@@ -397,16 +405,20 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, sections=None, interleaved
     if q is not None:
         qp, qs, hq = _head_rows("q", q, D)
         if q_out is None:
-            q_out = torch.empty((T, hq, D), dtype=torch.bfloat16, device=q.device)
-        _want(q_out.shape == q.shape, "q_out must have q's shape")
-        qo, qos, _ = _head_rows("q_out", q_out, D)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            qo, qos = q_out.data_ptr(), hq * D
+        else:
+            _want(q_out.shape == q.shape, "q_out must have q's shape")
+            qo, qos, _ = _head_rows("q_out", q_out, D)
     if k is not None:
         _want(k.shape[0] == T, "q and k need the same tokens")
         kp, ks, hk = _head_rows("k", k, D)
         if k_out is None:
-            k_out = torch.empty((T, hk, D), dtype=torch.bfloat16, device=k.device)
-        _want(k_out.shape == k.shape, "k_out must have k's shape")
-        ko, kos, _ = _head_rows("k_out", k_out, D)
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            ko, kos = k_out.data_ptr(), hk * D
+        else:
+            _want(k_out.shape == k.shape, "k_out must have k's shape")
+            ko, kos, _ = _head_rows("k_out", k_out, D)
     _check(lib.wlq_qk_norm_rope(qp, qs, hq, kp, ks, hk, T, D, _weight("q_weight", q_weight, D),
                                 _weight("k_weight", k_weight, D), eps, *_rope(positions, inv_freq, sections, T),
                                 int(interleaved), qo, qos, ko, kos, _stream(stream)))
@@ -416,25 +428,26 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, sections=None, interleaved
 def _pool(cache):
     """(pointers..., num_pages, page_size, group), heads, head_dim of a 4-bit cache."""
     kc, ks, vc, vs = cache
-    pages, H, P, half = kc.shape
-    groups = ks.shape[-1]
-    _want(kc.dtype == torch.uint8 and vc.dtype == torch.uint8 and ks.dtype == torch.float16 and vs.dtype == torch.float16,
-          "cache: uint8 codes and fp16 scales")
-    _want(vc.shape == kc.shape and vs.shape == ks.shape and ks.shape[:3] == kc.shape[:3] and groups > 0,
-          "cache: the arrays' shapes do not match")
-    _want(kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous(), "cache: contiguous arrays")
+    shape = kc.shape
+    pages, H, P, half = shape
+    scales = ks.shape
+    groups = scales[3]
+    if (kc.dtype is not torch.uint8 or vc.dtype is not torch.uint8 or ks.dtype is not torch.float16 or vs.dtype is not torch.float16
+            or vc.shape != shape or vs.shape != scales or scales != (pages, H, P, groups) or groups == 0):
+        raise WlqError(ERR_INVALID_ARG, "cache: uint8 codes [pages, heads, page_size, head_dim / 2] and fp16 scales "
+                                        "[pages, heads, page_size, head_dim / group], the same for keys and values")
+    if not (kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()):
+        raise WlqError(ERR_INVALID_ARG, "cache: contiguous arrays")
     return (kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages, P, 2 * half // groups), H, 2 * half
 
 
 def _batch(cu_seqlens, kv_lens, block_table, max_q: int):
-    _want(cu_seqlens.dtype == torch.int32 and kv_lens.dtype == torch.int32 and block_table.dtype == torch.int32,
-          "cu_seqlens, kv_lens and block_table must be int32")
-    n = kv_lens.numel()
-    _want(cu_seqlens.numel() == n + 1 and block_table.dim() == 2 and block_table.shape[0] == n,
-          "cu_seqlens [batch + 1], kv_lens [batch], block_table [batch, width]")
-    _want(cu_seqlens.is_contiguous() and kv_lens.is_contiguous() and block_table.is_contiguous(),
-          "cu_seqlens, kv_lens and block_table must be contiguous")
-    return cu_seqlens.data_ptr(), kv_lens.data_ptr(), n, int(max_q), block_table.data_ptr(), block_table.shape[1]
+    n, width = block_table.shape
+    i32 = torch.int32
+    if (cu_seqlens.dtype is not i32 or kv_lens.dtype is not i32 or block_table.dtype is not i32 or cu_seqlens.numel() != n + 1
+            or kv_lens.numel() != n or not (cu_seqlens.is_contiguous() and kv_lens.is_contiguous() and block_table.is_contiguous())):
+        raise WlqError(ERR_INVALID_ARG, "contiguous int32 cu_seqlens [batch + 1], kv_lens [batch], block_table [batch, width]")
+    return cu_seqlens.data_ptr(), kv_lens.data_ptr(), n, max_q, block_table.data_ptr(), width
 
 
 def kv4_append(cache, k, v, cu_seqlens, kv_lens, block_table, max_q: int, positions=None, inv_freq=None, sections=None,
@@ -446,10 +459,11 @@ def kv4_append(cache, k, v, cu_seqlens, kv_lens, block_table, max_q: int, positi
     bound of the sequences' token counts."""
     ptrs, H, D = _pool(cache)
     T = k.shape[0]
-    _want(v.shape == k.shape and k.shape[1] == H, "k and v must be [tokens, the cache's heads, head_dim]")
     _on(k, v, *cache, cu_seqlens, kv_lens, block_table, positions, inv_freq, k_weight)
-    kp, kst, _ = _head_rows("k", k, D)
-    vp, vst, _ = _head_rows("v", v, D)
+    kp, kst, hk = _head_rows("k", k, D)
+    vp, vst, hv = _head_rows("v", v, D)
+    if hk != H or hv != H or v.shape[0] != T:
+        raise WlqError(ERR_INVALID_ARG, "k and v must be [tokens, the cache's heads, head_dim]")
     _check(lib.wlq_kv4_append(kp, kst, vp, vst, T, H, D, _weight("k_weight", k_weight, D), eps,
                               *_rope(positions, inv_freq, sections, T), int(interleaved),
                               *_batch(cu_seqlens, kv_lens, block_table, max_q), *ptrs, _stream(stream)))
@@ -490,9 +504,10 @@ def kv4_attention(q, cache, cu_seqlens, kv_lens, block_table, max_q: int, max_kv
     _on(q, *cache, cu_seqlens, kv_lens, block_table, out, lse, workspace)
     qp, qs, _ = _head_rows("q", q, D)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    _want(out.shape == q.shape and out.dtype == torch.bfloat16 and out.is_contiguous(), "out must be contiguous bf16 of q's shape")
-    _want(lse is None or (lse.shape == (T, Hq) and lse.dtype == torch.float32 and lse.is_contiguous()),
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _want(out.shape == q.shape and out.dtype is torch.bfloat16 and out.is_contiguous(), "out must be contiguous bf16 of q's shape")
+    _want(lse is None or (lse.shape == (T, Hq) and lse.dtype is torch.float32 and lse.is_contiguous()),
           "lse must be contiguous fp32 [tokens, q_heads]")
     batch = _batch(cu_seqlens, kv_lens, block_table, max_q)
     if workspace is None:
@@ -500,18 +515,24 @@ def kv4_attention(q, cache, cu_seqlens, kv_lens, block_table, max_q: int, max_kv
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
     ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.wlq_kv4_attention(qp, qs, T, Hq, H, D, batch[0], batch[1], batch[2], batch[3], max_kv, batch[4], batch[5], *ptrs,
-                                 D ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), _ptr(lse),
-                                 _ptr(workspace), ws_n, _stream(stream)))
+                                 D ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(),
+                                 None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), ws_n,
+                                 _stream(stream)))
     return out
 
 
 def _int8_operands(y, wq, ws, bias, M: int, K: int):
-    N = wq.shape[0]
-    _want(wq.dtype == torch.int8 and wq.dim() == 2 and wq.shape[1] == K and wq.is_contiguous(), "wq must be contiguous int8 [N, K]")
-    _want(ws.dtype == torch.float32 and ws.numel() == N and ws.is_contiguous(), "ws must be contiguous fp32 [N]")
-    _want(bias is None or (bias.dtype == torch.bfloat16 and bias.numel() == N and bias.is_contiguous()), "bias must be contiguous bf16 [N]")
-    _want(y.dtype in (torch.bfloat16, torch.float32) and y.shape == (M, N) and y.is_contiguous(), "y must be contiguous bf16 or fp32 [M, N]")
-    return N, OUT_F32 if y.dtype == torch.float32 else OUT_BF16
+    N, Kw = wq.shape
+    if wq.dtype is not torch.int8 or Kw != K or not wq.is_contiguous():
+        raise WlqError(ERR_INVALID_ARG, "wq must be contiguous int8 [N, K]")
+    if ws.dtype is not torch.float32 or ws.numel() != N or not ws.is_contiguous():
+        raise WlqError(ERR_INVALID_ARG, "ws must be contiguous fp32 [N]")
+    if bias is not None and (bias.dtype is not torch.bfloat16 or bias.numel() != N or not bias.is_contiguous()):
+        raise WlqError(ERR_INVALID_ARG, "bias must be contiguous bf16 [N]")
+    dt = y.dtype
+    if (dt is not torch.bfloat16 and dt is not torch.float32) or y.shape != (M, N) or not y.is_contiguous():
+        raise WlqError(ERR_INVALID_ARG, "y must be contiguous bf16 or fp32 [M, N]")
+    return N, OUT_F32 if dt is torch.float32 else OUT_BF16
 
 
 def int8_linear_into(y, xq, xs, wq, ws, bias=None, stream=None):
@@ -522,7 +543,8 @@ def int8_linear_into(y, xq, xs, wq, ws, bias=None, stream=None):
     _want(xq.dtype == torch.int8 and xq.is_contiguous(), "xq must be contiguous int8 [M, K]")
     _want(xs.dtype == torch.float32 and xs.numel() == M and xs.is_contiguous(), "xs must be contiguous fp32 [M]")
     N, out = _int8_operands(y, wq, ws, bias, M, K)
-    _check(lib.wlq_int8_linear(_ptr(xq), _ptr(xs), M, _ptr(wq), _ptr(ws), N, K, _ptr(bias), _ptr(y), out, _stream(stream)))
+    _check(lib.wlq_int8_linear(xq.data_ptr(), xs.data_ptr(), M, wq.data_ptr(), ws.data_ptr(), N, K,
+                               None if bias is None else bias.data_ptr(), y.data_ptr(), out, _stream(stream)))
     return y
 
 
@@ -542,7 +564,8 @@ def w8a8_linear_into(y, x, wq, ws, bias=None, workspace=None, stream=None):
         n = int(lib.wlq_w8a8_workspace(M, K))
         workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
     ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib.wlq_w8a8_linear(_ptr(x), M, _ptr(wq), _ptr(ws), N, K, _ptr(bias), _ptr(y), out, _ptr(workspace), ws_n, _stream(stream)))
+    _check(lib.wlq_w8a8_linear(x.data_ptr(), M, wq.data_ptr(), ws.data_ptr(), N, K, None if bias is None else bias.data_ptr(),
+                               y.data_ptr(), out, None if workspace is None else workspace.data_ptr(), ws_n, _stream(stream)))
     return y
 
 
