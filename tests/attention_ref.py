@@ -87,7 +87,7 @@ def cache_values(codes, scales, pages, n):
 def attention(q, cache, cu, kv_lens, table, scale, causal, window):
     """The 64-bit attention and what its error bounds need: a dict of fp64 arrays
     out, lse, E (the largest score error of fp16 keys), A (sum_j p_j |v_j|), B
-    (2^-25 sum_j |v_j|).  Rows of no sequence are NaN; a query that sees
+    (2^-25 sum_j |q_j| max_j s_j, q and s the values' codes and scales).  Rows of no sequence are NaN; a query that sees
     nothing has out 0 and lse -inf."""
     T, Hq, D = q.shape
     dev = cache[0].device
@@ -103,6 +103,11 @@ def attention(q, cache, cu, kv_lens, table, scale, causal, window):
         rows, pages = slice(int(cu[b]), int(cu[b + 1])), table[b][: -(-kv // P)]
         k, v = cache_values(cache[0], cache[1], pages, kv), cache_values(cache[2], cache[3], pages, kv)
         there = ~torch.isnan(k[0, :, 0])
+        n_pages = torch.as_tensor(np.clip(np.asarray(pages, dtype=np.int64), 0, cache[0].shape[0] - 1), device=dev)
+        vs = cache[3][n_pages].double().transpose(0, 1).reshape(hk, -1, cache[3].shape[3])[:, :kv]  # [heads, kv, groups]
+        vs = torch.where(there[:, None], vs, 0.0).repeat_interleave(D // cache[3].shape[3], -1)
+        vq = torch.where(vs > 0, v.nan_to_num() / torch.where(vs > 0, vs, 1.0), 0.0)
+        b25 = 2.0 ** -25 * (vq.abs() * vs.amax((1, 2), keepdim=True)).sum(1)                           # [heads, D]
         k, v = torch.where(there[:, None], k, 0.0), torch.where(there[:, None], v, 0.0)
         i, j = torch.arange(n, device=dev)[:, None] + (kv - n), torch.arange(kv, device=dev)
         seen = torch.ones(n, kv, dtype=torch.bool, device=dev)
@@ -122,5 +127,5 @@ def attention(q, cache, cu, kv_lens, table, scale, causal, window):
             r["out"][rows, h], r["A"][rows, h] = p @ vh, p @ vh.abs()
             r["lse"][rows, h] = (torch.log(l) + top)[:, 0]
             r["E"][rows, h] = (q[rows, h].abs() @ kh.abs().T).amax(-1) * abs(scale) * (2.0 ** -11 + 2.0 ** -20)
-            r["B"][rows, h] = vh.abs().sum(0) * 2.0 ** -25
+            r["B"][rows, h] = b25[h // share]
     return {k: x.cpu().numpy() for k, x in r.items()}

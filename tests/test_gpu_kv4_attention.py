@@ -4,12 +4,13 @@ Bounds, from the roundings the header names.  Keys, values and weights enter
 the products as fp16 (2^-11 relative each), scores and sums are fp32, the
 output is rounded to bf16 (2^-8).  With E the largest possible score error of a
 query, max_j scale sum_d |q_d k_jd| (2^-11 + 2^-20), A = sum_j p_j |v_j| and
-B = 2^-25 sum_j |v_j|:
+B = 2^-25 sum_j |q_j| max_j s_j (q, s: the values' codes and scales):
     |out - ref| <= 2^-8 |ref| + (A (2 E + 2 * 2^-11 + 2^-16) + B) (1 + 2^-8),
     |lse - ref| <= E + 2^-16 max(1, |ref|)
 (a weight's relative error is at most e^(2 E) - 1 after normalising; a weight
 below 2^-14 of the running maximum's is an fp16 subnormal, whose half step is
-2^-25, and the sum the weights are divided by is at least 1: B; 2^-16
+2^-25, and the sum the weights are divided by is at least 1; where a weight
+carries its value's scale it is held against the largest scale: B; 2^-16
 covers ex2.approx and the fp32 sums of at most 2^16 terms' worth of rounding).
 For random values the errors average out: the 2-norm error stays below 2^-8
 of the result's (2^-8 / sqrt 3 from the output's rounding, 2^-11 each from the

@@ -131,6 +131,18 @@ DecPlan dec_plan(int64_t tokens, int batch, int max_q, int64_t max_kv, int q_hea
     return p;
 }
 
+template <int D, int NT, int G>
+cudaError_t launch_dec(unsigned grid, cudaStream_t s, const wlq::AttnArgs& a, DeviceInfo* d) {
+    constexpr size_t smem = wlq::dec_smem_bytes<D, NT, G>();
+    constexpr int kid = 28 + (D == 128 ? 8 : 0) + (NT == 2 ? 4 : 0) + (G == 4 ? 2 : G == 2 ? 1 : 0);  // 28..39
+    if (!d->smem_set[kid]) {
+        const cudaError_t e = cudaFuncSetAttribute(wlq::kv4_decode_kernel<D, NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        d->smem_set[kid] = true;
+    }
+    return launch_k(wlq::kv4_decode_kernel<D, NT, G>, grid, wlq::DEC_WARPS * 32, smem, s, a);
+}
+
 template <int D>
 wlq_status launch_attention(const wlq::AttnArgs& a, const DecPlan& p, DeviceInfo* d, cudaStream_t s) {
     const int64_t grid = static_cast<int64_t>(a.B.batch) * a.P.heads * p.row_tiles * p.splits;
@@ -145,9 +157,13 @@ wlq_status launch_attention(const wlq::AttnArgs& a, const DecPlan& p, DeviceInfo
             d->smem_set[kid] = true;
         }
         e = launch_k(wlq::kv4_chunk_kernel<D>, gx, wlq::CH_THREADS, wlq::ch_smem_bytes<D>(), s, a, kDefaultTimeoutNs);
-    } else
-    e = p.nt == 1 ? launch_k(wlq::kv4_decode_kernel<D, 1>, gx, wlq::DEC_WARPS * 32, 0, s, a)
-                              : launch_k(wlq::kv4_decode_kernel<D, 2>, gx, wlq::DEC_WARPS * 32, 0, s, a);
+    } else if (D >> a.P.lg_group == 4) {
+        e = p.nt == 1 ? launch_dec<D, 1, 4 * D / 128>(gx, s, a, d) : launch_dec<D, 2, 4 * D / 128>(gx, s, a, d);
+    } else if (D >> a.P.lg_group == 2) {
+        e = p.nt == 1 ? launch_dec<D, 1, 2>(gx, s, a, d) : launch_dec<D, 2, 2>(gx, s, a, d);
+    } else {
+        e = p.nt == 1 ? launch_dec<D, 1, 1>(gx, s, a, d) : launch_dec<D, 2, 1>(gx, s, a, d);
+    }
     if (e == cudaSuccess && p.splits > 1) {
         const int64_t units = cdiv(static_cast<int64_t>(a.B.batch) * a.B.max_q * a.q_heads, 8);
         if (units >= (int64_t(1) << 31)) return fail(WLQ_ERR_SHAPE, "too many queries in one call");

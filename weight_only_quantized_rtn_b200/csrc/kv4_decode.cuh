@@ -6,24 +6,30 @@
 // Everything is transposed, so that the cache is the 16-row operand of
 // mma.sync m16n8k16 and no row of it is wasted:
 //   S^T [16 tokens x 8 rows] = K [16 x D] Q^T,   O^T [16 inputs x 8 rows] += V^T [16 x 16 tokens] P^T.
-// A lane reads K as one run of D / 4 codes of two tokens, V as runs of D / 8
-// codes of four tokens: the inner dimensions of both products are renumbered
-// to what a lane's run holds, so codes go from global memory to MMA operands
-// without shared memory.  P^T moves from accumulator to operand layout by one
-// movmatrix per 8 x 8 block.
 //
-// A pair of codes becomes two fp16 by one mask-or (1024 + u, or 1024 + 16 u)
-// and one exact subtraction or fma, then one product with the scale: fp16 of
-// code * scale, one rounding (2^-11).  Weights exp(x - m) are fp16 (2^-11);
-// scores, m, l and the outputs are fp32.
-// m follows the running maximum lazily: it is moved only when a score exceeds
-// it by more than 8 (in powers of two), so weights stay below 2^8 and most
-// steps need one vote instead of a reduction and a rescaling.
+// The products take the CODES, as exact fp16; no scale is applied to them:
+//  - K: 16 bytes of a row are 32 inputs of one group (groups are 32 and more),
+//    so the scores of each group are accumulated apart and scaled in fp32;
+//  - V: an MMA's 16 outputs lie in one such block too, so the scale goes into
+//    the weights: P' = 2^(x - M) vs, one fp16 rounding (2^-11).  The reference
+//    M is the running maximum of the scores plus the exponent E of the largest
+//    V scale so far, so P' stays below 2^9 whatever the scales are; l is summed
+//    with the same M and cancels it.
+// ldmatrix hands a lane word t of 16 bytes of row g (K), and with .trans the
+// 16-bit pieces of two tokens side by side (V): four inputs of a token pair,
+// one mask-or and one exact fp16 operation from the MMA's operand.  P^T moves
+// from accumulator to operand layout by one movmatrix per 8 x 8 block.
+// The maximum is moved lazily: only when a score exceeds it by more than 8 (in
+// powers of two), or E grows; most steps need one vote instead of a reduction
+// and a rescaling.
 //
-// Bound: HBM (each cached byte once).  One warp holds a unit of 32 tokens in
-// flight while it works on the one before; 4 warps share a CTA's part of the
-// sequence, and long sequences are split over CTAs whose partial (m, l, O)
-// kv4_combine_kernel joins in split order.
+// Bound: HBM (each cached byte once); next to it the instruction issue, about
+// 480 instructions a warp for 32 tokens of D = 128, where HBM's rate leaves
+// 700.  A warp keeps three units of 32 tokens in a ring of its own in shared
+// memory (cp.async, 16-byte pieces permuted so that ldmatrix meets no bank
+// twice); 4 warps share a CTA's part of the sequence, and long sequences are
+// split over CTAs whose partial (M, l, O) kv4_combine_kernel joins in split
+// order.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -97,92 +103,116 @@ __device__ __forceinline__ float pow2f(int e) {  // 2^e for e in [-252, 252]: tw
     return __uint_as_float(static_cast<uint32_t>(127 + h) << 23) * __uint_as_float(static_cast<uint32_t>(127 + e - h) << 23);
 }
 
-template <int D>
-struct DecUnit {  // one unit's codes and scales of a lane
-    static constexpr int KW = D / 32;  // words of a K run
-    static constexpr int VW = D / 64;  // words of a V run
-    uint32_t k[4][KW];  // rows g, g + 8 of the two 16-token tiles
-    uint32_t v[8][VW];  // tokens 2t, 2t+1, 2t+8, 2t+9 of each tile
-    __half ks[4], vs[8];
-    bool ok[2];  // the tile's page is in range
-};
+// 16 bytes from global to shared memory, asynchronously.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// Four pairs of nibbles of w (nibble i of each half) as fp16 codes, exact.
+__device__ __forceinline__ void nibbles_codes(uint32_t w, uint32_t (&o)[4]) {
+    const __half2 k1032 = bits_h2(0x64086408u), k16 = bits_h2(0x2C002C00u), k72 = bits_h2(0xD480D480u);  // 1032, 1/16, -72
+    const uint32_t v = w >> 8;
+    o[0] = h2_bits(__hsub2(bits_h2((w & 0x000F000Fu) | 0x64006400u), k1032));
+    o[1] = h2_bits(__hfma2(bits_h2((w & 0x00F000F0u) | 0x64006400u), k16, k72));
+    o[2] = h2_bits(__hsub2(bits_h2((v & 0x000F000Fu) | 0x64006400u), k1032));
+    o[3] = h2_bits(__hfma2(bits_h2((v & 0x00F000F0u) | 0x64006400u), k16, k72));
+}
 
-template <int D>
-__device__ __forceinline__ void dec_pages(const AttnArgs& a, int b, int unit, int end, int (&pg)[2]) {
+constexpr int DEC_STAGES = 3;
+template <int D, int G>  // G groups a row
+struct DecRing {
+    static constexpr int ROW = D / 2;                  // bytes of a row's codes
+    static constexpr int CODES = DEC_UNIT * ROW;       // of a unit's codes of K or V
+    static constexpr int SCALES = DEC_UNIT * G * 2;
+    static constexpr int STAGE = 2 * CODES + 2 * SCALES;  // K codes, V codes, K scales, V scales
+    static constexpr int BYTES = DEC_WARPS * DEC_STAGES * STAGE;
+    // Place of 16-byte piece c of row r: eight rows' same piece lie in eight different bank groups.
+    static __device__ __forceinline__ uint32_t at(int r, int c) {
+        if constexpr (D == 128) return r * ROW + ((c ^ ((r >> 1) & 3)) << 4);
+        else return r * ROW + ((c ^ ((r >> 2) & 1)) << 4);
+    }
+};
+template <int D, int NT>
+__host__ __device__ constexpr size_t dec_out_bytes() { return static_cast<size_t>(DEC_WARPS) * 8 * NT * (D + 4) * 4 + DEC_WARPS * 8 * NT * 8; }
+template <int D, int NT, int G>
+__host__ __device__ constexpr size_t dec_smem_bytes() {
+    return DecRing<D, G>::BYTES > dec_out_bytes<D, NT>() ? DecRing<D, G>::BYTES : dec_out_bytes<D, NT>();
+}
+
+// Pages of a unit's two 16-token tiles (0xFFFFFFFF: no token of the range, or out of range).
+__device__ __forceinline__ void dec_pages(const AttnArgs& a, const int32_t* table, int unit, int ue, int end, uint32_t (&pg)[2]) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const int tok = unit * DEC_UNIT + 16 * t;
-        pg[t] = -1;
-        if (tok < end) {  // a tile with a token of the range
-            const int64_t e = tok >> a.P.page_shift;
-            if (e < a.B.table_stride) pg[t] = a.B.table[b * a.B.table_stride + e];
-            if (!kv_page_ok(pg[t], a.P.pages)) {
-                raise_error(ERRBIT_INDEX);
-                pg[t] = -1;
-            }
-        }
+        const int tok = unit * DEC_UNIT + 16 * t, e = tok >> a.P.page_shift;
+        pg[t] = 0xFFFFFFFFu;
+        if (unit < ue && tok < end && e < a.B.table_stride) pg[t] = static_cast<uint32_t>(__ldg(table + e));
     }
 }
 
-template <int D>
-__device__ __forceinline__ void dec_load(const AttnArgs& a, int h, int unit, const int (&pg)[2], int lane, DecUnit<D>& u) {
-    const int g = lane >> 2, t = lane & 3;
-    const int lg = a.P.lg_group, gpr = D >> lg;  // groups of a row
+// A unit's codes and scales on their way into a stage.
+template <int D, int G>
+__device__ __forceinline__ void dec_fetch(const AttnArgs& a, int h, int unit, const uint32_t (&pg)[2], int lane, uint32_t stage) {
+    using R = DecRing<D, G>;
+    constexpr int CPR = D / 32;      // pieces of a row
+    constexpr int RPI = 32 / CPR;    // rows of one instruction
+    const uint32_t npages = static_cast<uint32_t>(a.P.pages);
+    int64_t row[2];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-        u.ok[m] = pg[m] >= 0;
-        const int place = (unit * DEC_UNIT + 16 * m) & ((1 << a.P.page_shift) - 1);
-        const int64_t row = ((static_cast<int64_t>(max(pg[m], 0)) * a.P.heads + h) << a.P.page_shift) + place;
-        if (u.ok[m]) {
+    for (int t = 0; t < 2; ++t)
+        row[t] = ((static_cast<int64_t>(pg[t]) * a.P.heads + h) << a.P.page_shift) + ((unit * DEC_UNIT + 16 * t) & ((1 << a.P.page_shift) - 1));
+    const int c = lane % CPR, r0 = lane / CPR;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint8_t* p = a.P.k + (row + g + 8 * r) * (D / 2) + t * (D / 8);
-                if constexpr (D == 128) {
-                    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
-                    u.k[2 * m + r][0] = x.x; u.k[2 * m + r][1] = x.y; u.k[2 * m + r][2] = x.z; u.k[2 * m + r][3] = x.w;
-                } else {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-                    u.k[2 * m + r][0] = x.x; u.k[2 * m + r][1] = x.y;
-                }
-                u.ks[2 * m + r] = a.P.ks[(row + g + 8 * r) * gpr + ((t * (D / 4)) >> lg)];
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int64_t vr = row + 2 * t + (r & 1) + 8 * (r >> 1);
-                const uint8_t* p = a.P.v + vr * (D / 2) + g * (D / 16);
-                if constexpr (D == 128) {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-                    u.v[4 * m + r][0] = x.x; u.v[4 * m + r][1] = x.y;
-                } else {
-                    u.v[4 * m + r][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-                }
-                u.vs[4 * m + r] = a.P.vs[vr * gpr + ((g * (D / 8)) >> lg)];
-            }
-        } else {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-#pragma unroll
-                for (int w = 0; w < D / 32; ++w) u.k[2 * m + r][w] = 0x88888888u;
-                u.ks[2 * m + r] = __float2half_rn(0.0f);
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-#pragma unroll
-                for (int w = 0; w < D / 64; ++w) u.v[4 * m + r][w] = 0x88888888u;
-                u.vs[4 * m + r] = __float2half_rn(0.0f);
-            }
+    for (int i = 0; i < DEC_UNIT / RPI; ++i) {
+        const int r = r0 + i * RPI, t = (i * RPI) >> 4;  // an instruction's rows lie in one tile
+        if (pg[t] < npages) {
+            const int64_t at = (row[t] + (r & 15)) * R::ROW + c * 16;
+            cp_async16(stage + R::at(r, c), a.P.k + at);
+            cp_async16(stage + R::CODES + R::at(r, c), a.P.v + at);
         }
+    }
+    if (lane < 8 * G) {
+        const int which = lane / (4 * G), idx = lane % (4 * G), t = idx / (2 * G), off = idx % (2 * G);
+        if ((t ? pg[1] : pg[0]) < npages)
+            cp_async16(stage + 2 * R::CODES + which * R::SCALES + idx * 16,
+                       reinterpret_cast<const uint8_t*>((which ? a.P.vs : a.P.ks) + (t ? row[1] : row[0]) * G) + off * 16);
     }
 }
 
-// Cached rows that were never written may hold any bits: a NaN or infinite
-// scale there would survive a weight of zero, so unseen tokens' V scales are
-// zeroed with their weights.
-template <int D, int NT>
-__global__ void __launch_bounds__(DEC_WARPS * 32) kv4_decode_kernel(const AttnArgs a) {
-    constexpr int KS = D / 16;  // 16-input steps of the scores, 16-input tiles of the outputs
-    __shared__ float sm_o[DEC_WARPS][8 * NT][D + 4];
-    __shared__ float2 sm_ml[DEC_WARPS][8 * NT];
+// G fp16 scales of one token.
+template <int G>
+__device__ __forceinline__ void load_scales(const uint8_t* p, __half (&s)[G]) {
+    if constexpr (G == 1) {
+        s[0] = *reinterpret_cast<const __half*>(p);
+    } else if constexpr (G == 2) {
+        const __half2 x = *reinterpret_cast<const __half2*>(p);
+        s[0] = __low2half(x); s[1] = __high2half(x);
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        s[0] = __low2half(bits_h2(u.x)); s[1] = __high2half(bits_h2(u.x));
+        s[2] = __low2half(bits_h2(u.y)); s[3] = __high2half(bits_h2(u.y));
+    }
+}
+
+template <int D, int NT, int G>
+__global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_kernel(const AttnArgs a) {
+    using R = DecRing<D, G>;
+    constexpr int W = D / 32;           // 32-input blocks of a row
+    constexpr int BPG = W / G;          // blocks of a group
+    extern __shared__ __align__(128) uint8_t dec_smem[];
     grid_dependency_sync();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     int idx = blockIdx.x;
@@ -209,23 +239,37 @@ __global__ void __launch_bounds__(DEC_WARPS * 32) kv4_decode_kernel(const AttnAr
     const int ub = u0 + static_cast<int>(static_cast<int64_t>(units) * split / a.splits);
     const int ue = u0 + static_cast<int>(static_cast<int64_t>(units) * (split + 1) / a.splits);
 
-    // queries: row 8 nt + g, inputs t D/4 + 4 j .. + 3 for step j
-    uint32_t qf[NT][KS][2];
+    // the first units on their way
+    const uint32_t ring = smem_u32(dec_smem) + warp * DEC_STAGES * R::STAGE;
+    const int32_t* table = a.B.table + b * a.B.table_stride;
+    const uint32_t npages = static_cast<uint32_t>(a.P.pages);
+    uint32_t pg[DEC_STAGES][2];  // pages of the units in flight, in order
+#pragma unroll
+    for (int i = 0; i < DEC_STAGES; ++i) dec_pages(a, table, ub + warp + i * DEC_WARPS, ue, hi, pg[i]);
+#pragma unroll
+    for (int i = 0; i < DEC_STAGES - 1; ++i) {
+        dec_fetch<D, G>(a, h, ub + warp + i * DEC_WARPS, pg[i], lane, ring + i * R::STAGE);
+        cp_async_commit();
+    }
+
+    // queries: row 8 nt + g; in 32-input block w, lane t has inputs 8 t .. 8 t + 7 of the block
+    uint32_t qf[NT][2 * W][2];
     float cs[NT][2];  // score factor of this lane's accumulator columns (rows 8 nt + 2 t, + 1)
     int clo[NT][2], chi[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int row = row0 + 8 * nt + g;
-        uint2 raw[KS];
+        uint4 raw[W];
         uint32_t m2 = 0;
 #pragma unroll
-        for (int j = 0; j < KS; ++j) raw[j] = make_uint2(0u, 0u);
+        for (int w = 0; w < W; ++w) raw[w] = make_uint4(0u, 0u, 0u, 0u);
         if (row < rows) {
-            const uint16_t* p = a.q + (r0 + row / a.share) * a.q_stride + static_cast<int64_t>(h * a.share + row % a.share) * D + t * (D / 4);
+            const uint16_t* p = a.q + (r0 + row / a.share) * a.q_stride + static_cast<int64_t>(h * a.share + row % a.share) * D + 8 * t;
 #pragma unroll
-            for (int j = 0; j < KS; ++j) {
-                raw[j] = *reinterpret_cast<const uint2*>(p + 4 * j);
-                m2 = __vmaxu2(m2, __vmaxu2(raw[j].x & 0x7FFF7FFFu, raw[j].y & 0x7FFF7FFFu));
+            for (int w = 0; w < W; ++w) {
+                raw[w] = *reinterpret_cast<const uint4*>(p + 32 * w);
+                m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(raw[w].x & 0x7FFF7FFFu, raw[w].y & 0x7FFF7FFFu),
+                                           __vmaxu2(raw[w].z & 0x7FFF7FFFu, raw[w].w & 0x7FFF7FFFu)));
             }
         }
         uint32_t mx = max(m2 & 0xFFFFu, m2 >> 16);
@@ -234,9 +278,11 @@ __global__ void __launch_bounds__(DEC_WARPS * 32) kv4_decode_kernel(const AttnAr
         const int e = row_exponent(mx);
         const float f = pow2f(e);
 #pragma unroll
-        for (int j = 0; j < KS; ++j) {
-            qf[nt][j][0] = h2_bits(__floats2half2_rn(__uint_as_float(raw[j].x << 16) * f, __uint_as_float(raw[j].x & 0xFFFF0000u) * f));
-            qf[nt][j][1] = h2_bits(__floats2half2_rn(__uint_as_float(raw[j].y << 16) * f, __uint_as_float(raw[j].y & 0xFFFF0000u) * f));
+        for (int w = 0; w < W; ++w) {
+            const uint32_t x[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                qf[nt][2 * w + k / 2][k & 1] = h2_bits(__floats2half2_rn(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xFFFF0000u) * f));
         }
         const float c = a.scale_log2 * pow2f(-e);
 #pragma unroll
@@ -246,7 +292,9 @@ __global__ void __launch_bounds__(DEC_WARPS * 32) kv4_decode_kernel(const AttnAr
             seen_range(a, kv - n + cr / a.share, kv, clo[nt][k], chi[nt][k]);
         }
     }
-    float m[NT][2], l[NT][2], o[NT][KS][4];
+    // m: running maximum of the scores, ev: exponent of the largest V scale so far; M = m + ev
+    float m[NT][2], l[NT][2], o[NT][2 * W][4], ev = -24.0f;
+    uint32_t vtop = 0;  // fp16 bits of 2^ev's upper end: a larger scale moves ev
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -255,131 +303,191 @@ __global__ void __launch_bounds__(DEC_WARPS * 32) kv4_decode_kernel(const AttnAr
             l[nt][k] = 0.0f;
         }
 #pragma unroll
-        for (int d = 0; d < KS; ++d)
+        for (int d = 0; d < 2 * W; ++d)
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[nt][d][k] = 0.0f;
     }
 
-    DecUnit<D> cur, nxt;
-    int pg[2], pn[2];
-    int u = ub + warp;
-    if (u < ue) {
-        dec_pages<D>(a, b, u, hi, pg);
-        dec_load<D>(a, h, u, pg, lane, cur);
-        if (u + DEC_WARPS < ue) dec_pages<D>(a, b, u + DEC_WARPS, hi, pn);
-    }
-    for (; u < ue; u += DEC_WARPS) {
-        if (u + DEC_WARPS < ue) {
-            dec_load<D>(a, h, u + DEC_WARPS, pn, lane, nxt);
-            if (u + 2 * DEC_WARPS < ue) dec_pages<D>(a, b, u + 2 * DEC_WARPS, hi, pn);
+    // ldmatrix rows of this lane.  K, D = 128: matrices are the blocks 0..3 of 8 rows; D = 64: blocks 0, 1 of
+    // rows 0..7, then of rows 8..15.  V: blocks (2 i, tokens 0..7), (2 i, 8..15), (2 i + 1, ...), ...
+    const int mat = lane >> 3, mr = lane & 7;
+    int stage = 0;
+    for (int u = ub + warp; u < ue; u += DEC_WARPS) {
+        // the unit two ahead, into the stage read last
+        {
+            const int ahead = u + (DEC_STAGES - 1) * DEC_WARPS, st = stage == 0 ? DEC_STAGES - 1 : stage - 1;
+            if (ahead < ue) dec_fetch<D, G>(a, h, ahead, pg[DEC_STAGES - 1], lane, ring + st * R::STAGE);
+            cp_async_commit();
         }
+        cp_async_wait<DEC_STAGES - 1>();
+        __syncwarp();
+        const uint32_t sk = ring + stage * R::STAGE, sv = sk + R::CODES;
+        const uint8_t* sc = dec_smem + (sk - smem_u32(dec_smem)) + 2 * R::CODES;
         const int tok0 = u * DEC_UNIT;
-        const bool inside = tok0 >= lo_all && tok0 + DEC_UNIT <= hi_all && cur.ok[0] && cur.ok[1];
-        float s[2][NT][4];
+        const bool in0 = pg[0][0] < npages, in1 = pg[0][1] < npages;
+        const bool inside = tok0 >= lo_all && tok0 + DEC_UNIT <= hi_all && in0 && in1;
+        if (!inside && ((!in0 && tok0 < hi) || (!in1 && tok0 + 16 < hi)) && lane == 0) raise_error(ERRBIT_INDEX);
+        float x[2][NT][4];
+        __half vs[2][2][G];
+        uint32_t vmax = 0;
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
+            float acc[NT][G][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) s[mt][nt][k] = 0.0f;
-            const __half2 sa = __half2half2(cur.ks[2 * mt]), sb = __half2half2(cur.ks[2 * mt + 1]);
+                for (int i = 0; i < G; ++i)
 #pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
+                    for (int k = 0; k < 4; ++k) acc[nt][i][k] = 0.0f;
+            uint32_t kr[2][W];  // words t of the row's blocks, rows g and g + 8
+            if constexpr (D == 128) {
+                uint32_t q0[4], q1[4];
+                ldsm_x4(sk + R::at(16 * mt + mr, mat), q0);
+                ldsm_x4(sk + R::at(16 * mt + 8 + mr, mat), q1);
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    kr[0][w] = q0[w];
+                    kr[1][w] = q1[w];
+                }
+            } else {
+                uint32_t q[4];
+                ldsm_x4(sk + R::at(16 * mt + 8 * (mat >> 1) + mr, mat & 1), q);
+                kr[0][0] = q[0]; kr[0][1] = q[1]; kr[1][0] = q[2]; kr[1][1] = q[3];
+            }
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
                 uint32_t fa[4], fb[4];
-                nibbles_f16(cur.k[2 * mt][w], sa, fa);
-                nibbles_f16(cur.k[2 * mt + 1][w], sb, fb);
+                nibbles_codes(kr[0][w], fa);
+                nibbles_codes(kr[1][w], fb);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma16816_f16(s[mt][nt], fa[0], fb[0], fa[1], fb[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
-                    mma16816_f16(s[mt][nt], fa[2], fb[2], fa[3], fb[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+                    mma16816_f16(acc[nt][w / BPG], fa[0], fb[0], fa[1], fb[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
+                    mma16816_f16(acc[nt][w / BPG], fa[2], fb[2], fa[3], fb[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
                 }
             }
+            __half ks[2][G];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int tk = 16 * mt + 8 * r + g;
+                load_scales<G>(sc + tk * G * 2, ks[r]);
+                load_scales<G>(sc + R::SCALES + tk * G * 2, vs[mt][r]);
+                const bool there = inside || (tok0 + tk < kv && (mt ? in1 : in0));  // places no token was written to may hold anything
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    if (!there) vs[mt][r][i] = __ushort_as_half(0);
+                    vmax = max(vmax, static_cast<uint32_t>(__half_as_ushort(vs[mt][r][i])));
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float s = acc[nt][0][k] * __half2float(ks[k >> 1][0]);
+#pragma unroll
+                    for (int i = 1; i < G; ++i) s = fmaf(acc[nt][i][k], __half2float(ks[k >> 1][i]), s);
+                    x[mt][nt][k] = s * cs[nt][k & 1];
+                }
         }
-        bool move = false;
+        if (!inside) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int tok = tok0 + 16 * mt + 8 * (k >> 1) + g;
+                        if (tok < clo[nt][k & 1] || tok >= chi[nt][k & 1] || !(mt ? in1 : in0)) x[mt][nt][k] = -INFINITY;
+                    }
+        }
+        bool move = vmax > vtop;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float top = -INFINITY;
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        float x = s[mt][nt][2 * r + k] * cs[nt][k];
-                        if (!inside) {
-                            const int tok = tok0 + 16 * mt + 8 * r + g;
-                            if (tok < clo[nt][k] || tok >= chi[nt][k] || !cur.ok[mt]) x = -INFINITY;
-                        }
-                        s[mt][nt][2 * r + k] = x;
-                        top = fmaxf(top, x);
-                    }
-                move |= top > m[nt][k] + ATT_LAZY;
-            }
+            for (int k = 0; k < 2; ++k)
+                move |= fmaxf(fmaxf(x[0][nt][k], x[0][nt][2 + k]), fmaxf(x[1][nt][k], x[1][nt][2 + k])) > m[nt][k] + ATT_LAZY;
         if (__any_sync(0xffffffffu, move)) {
+            // a new reference: the largest scores, the exponent of the largest V scale
+            vmax = __reduce_max_sync(0xffffffffu, vmax);
+            float step = 0.0f;
+            if (vmax > vtop) {
+                vtop = vmax | 0x03FFu;  // up to the next power of two (subnormals: 2^-14)
+                const float en = static_cast<float>(max(static_cast<int>(vtop >> 10), 1) - 15);
+                step = en - ev;
+                ev = en;
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    float top = fmaxf(fmaxf(s[0][nt][k], s[0][nt][2 + k]), fmaxf(s[1][nt][k], s[1][nt][2 + k]));
+                    float top = fmaxf(fmaxf(x[0][nt][k], x[0][nt][2 + k]), fmaxf(x[1][nt][k], x[1][nt][2 + k]));
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
                     const float mn = fmaxf(m[nt][k], top);
-                    const float f = mn == -INFINITY ? 1.0f : ex2(m[nt][k] - mn);
+                    const float f = mn == -INFINITY ? 1.0f : ex2(m[nt][k] - mn - step);
                     m[nt][k] = mn;
                     l[nt][k] *= f;
 #pragma unroll
-                    for (int d = 0; d < KS; ++d) {
+                    for (int d = 0; d < 2 * W; ++d) {
                         o[nt][d][k] *= f;
                         o[nt][d][2 + k] *= f;
                     }
                 }
         }
-        uint32_t pf[2][NT][2];
+        // weights, then by groups: P' = weight * V scale as the operand of both token halves
+        uint32_t pf[2][NT][G][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+            float M[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) M[k] = m[nt][k] == -INFINITY ? 0.0f : m[nt][k] + ev;  // nothing seen yet: x is -inf too
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    float p[2];
+                    const float p0 = ex2(x[mt][nt][2 * r] - M[0]), p1 = ex2(x[mt][nt][2 * r + 1] - M[1]);
+                    l[nt][0] += p0;
+                    l[nt][1] += p1;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float base = m[nt][k] == -INFINITY ? 0.0f : m[nt][k];  // nothing seen yet: x is -inf too
-                        p[k] = ex2(s[mt][nt][2 * r + k] - base);
-                        l[nt][k] += p[k];
+                    for (int i = 0; i < G; ++i) {
+                        const float v = __half2float(vs[mt][r][i]);
+                        pf[mt][nt][i][r] = movmatrix(h2_bits(__floats2half2_rn(p0 * v, p1 * v)));
                     }
-                    pf[mt][nt][r] = movmatrix(h2_bits(__floats2half2_rn(p[0], p[1])));
                 }
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-            if (!inside) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int tok = tok0 + 16 * mt + 2 * t + (r & 1) + 8 * (r >> 1);
-                    if (tok >= kv) cur.vs[4 * mt + r] = __float2half_rn(0.0f);
-                }
-            }
-            const __half2 sab = __halves2half2(cur.vs[4 * mt], cur.vs[4 * mt + 1]);
-            const __half2 scd = __halves2half2(cur.vs[4 * mt + 2], cur.vs[4 * mt + 3]);
-#pragma unroll
-            for (int w = 0; w < D / 64; ++w) {
-                uint32_t ae[4], ao[4], ce[4], co[4];  // even / odd inputs of token pairs (2t, 2t+1), (2t+8, 2t+9)
-                const uint32_t va = cur.v[4 * mt][w], vb = cur.v[4 * mt + 1][w], vc = cur.v[4 * mt + 2][w], vd = cur.v[4 * mt + 3][w];
-                nibbles_f16(__byte_perm(va, vb, 0x5410), sab, ae);
-                nibbles_f16(__byte_perm(va, vb, 0x7632), sab, ao);
-                nibbles_f16(__byte_perm(vc, vd, 0x5410), scd, ce);
-                nibbles_f16(__byte_perm(vc, vd, 0x7632), scd, co);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16816_f16(o[nt][4 * w + i], ae[i], ao[i], ce[i], co[i], pf[mt][nt][0], pf[mt][nt][1]);
-            }
         }
-        cur = nxt;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int w2 = 0; w2 < W / 2; ++w2) {
+                uint32_t vr[4];  // block 2 w2: tokens 0..7, 8..15; block 2 w2 + 1
+                ldsm_x4_trans(sv + R::at(16 * mt + 8 * (mat & 1) + mr, 2 * w2 + (mat >> 1)), vr);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int w = 2 * w2 + j;
+                    uint32_t fa[4], fb[4];
+                    nibbles_codes(vr[2 * j], fa);
+                    nibbles_codes(vr[2 * j + 1], fb);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma16816_f16(o[nt][2 * w], fa[0], fa[1], fb[0], fb[1], pf[mt][nt][w / BPG][0], pf[mt][nt][w / BPG][1]);
+                        mma16816_f16(o[nt][2 * w + 1], fa[2], fa[3], fb[2], fb[3], pf[mt][nt][w / BPG][0], pf[mt][nt][w / BPG][1]);
+                    }
+                }
+            }
+        __syncwarp();  // the stage may be written again
+        stage = stage == DEC_STAGES - 1 ? 0 : stage + 1;
+#pragma unroll
+        for (int i = 0; i + 1 < DEC_STAGES; ++i) {
+            pg[i][0] = pg[i + 1][0];
+            pg[i][1] = pg[i + 1][1];
+        }
+        dec_pages(a, table, u + DEC_STAGES * DEC_WARPS, ue, hi, pg[DEC_STAGES - 1]);
     }
 
-    // the warps' parts, then the CTA's
+    // the warps' parts, then the CTA's (over the rings)
+    cp_async_wait<0>();
+    __syncthreads();
+    float* sm_o = reinterpret_cast<float*>(dec_smem);                                       // [warps][8 NT][D + 4]
+    float2* sm_ml = reinterpret_cast<float2*>(dec_smem + static_cast<size_t>(DEC_WARPS) * 8 * NT * (D + 4) * 4);  // [warps][8 NT]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -387,22 +495,24 @@ __global__ void __launch_bounds__(DEC_WARPS * 32) kv4_decode_kernel(const AttnAr
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], off);
             const int r = 8 * nt + 2 * t + k;
-            if (g == 0) sm_ml[warp][r] = make_float2(m[nt][k], l[nt][k]);
+            if (g == 0) sm_ml[warp * 8 * NT + r] = make_float2(m[nt][k] + ev, l[nt][k]);
 #pragma unroll
-            for (int d = 0; d < KS; ++d) {  // tile d: word d / 4, nibble d % 4 of the run of row g
-                const int at = g * (D / 8) + 8 * (d / 4) + 2 * (d % 4);
-                *reinterpret_cast<float2*>(&sm_o[warp][r][at]) = make_float2(o[nt][d][k], o[nt][d][2 + k]);
+            for (int d = 0; d < 2 * W; ++d) {  // block d / 2: nibbles 2 (d & 1) and 2 (d & 1) + 1 of 16-bit piece g
+                const int at = 32 * (d / 2) + 8 * (g >> 1) + 4 * (d & 1) + (g & 1);
+                float* dst = sm_o + (warp * 8 * NT + r) * (D + 4) + at;
+                dst[0] = o[nt][d][k];
+                dst[2] = o[nt][d][2 + k];
             }
         }
     __syncthreads();
     for (int r = warp; r < 8 * NT && row0 + r < rows; r += DEC_WARPS) {
         float M = -INFINITY, L = 0.0f, w[DEC_WARPS];
 #pragma unroll
-        for (int i = 0; i < DEC_WARPS; ++i) M = fmaxf(M, sm_ml[i][r].x);
+        for (int i = 0; i < DEC_WARPS; ++i) M = fmaxf(M, sm_ml[i * 8 * NT + r].x);
 #pragma unroll
         for (int i = 0; i < DEC_WARPS; ++i) {
-            w[i] = M == -INFINITY ? 0.0f : ex2(sm_ml[i][r].x - M);
-            L += w[i] * sm_ml[i][r].y;
+            w[i] = M == -INFINITY ? 0.0f : ex2(sm_ml[i * 8 * NT + r].x - M);
+            L += w[i] * sm_ml[i * 8 * NT + r].y;
         }
         const int64_t head_row = (r0 + (row0 + r) / a.share) * a.q_heads + h * a.share + (row0 + r) % a.share;
         const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);  // a NaN stays one
@@ -411,9 +521,9 @@ __global__ void __launch_bounds__(DEC_WARPS * 32) kv4_decode_kernel(const AttnAr
             float2 v = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int i = 0; i < DEC_WARPS; ++i) {
-                const float2 x = *reinterpret_cast<const float2*>(&sm_o[i][r][d]);
-                v.x += w[i] * x.x;
-                v.y += w[i] * x.y;
+                const float2 y = *reinterpret_cast<const float2*>(sm_o + (i * 8 * NT + r) * (D + 4) + d);
+                v.x += w[i] * y.x;
+                v.y += w[i] * y.y;
             }
             if (a.splits == 1) {
                 const __nv_bfloat162 y = __floats2bfloat162_rn(v.x * inv, v.y * inv);
