@@ -119,9 +119,12 @@ DecPlan dec_plan(int64_t tokens, int batch, int max_q, int64_t max_kv, int q_hea
         // one CTA an SM: split where the row tiles leave half of them idle, four steps a part at least
         p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms / base, units / 4, 32})));
     } else {
-    // enough CTAs for four on each SM, but at least two units for each warp of a split
-    const int64_t want = cdiv(4ll * sms, base), most = std::max<int64_t>(1, units / (2 * wlq::DEC_WARPS));
-    p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, 128})));
+        // Many sequences: about three rounds of four CTAs an SM, so that ragged ones even out, with at least four
+        // units for each warp of a part.  Few: one round (37 parts a head against 111 took 85 us against 100 for two
+        // sequences of up to 131072 tokens), with two units for each warp.
+        const int64_t want = base >= sms ? std::min(cdiv(12ll * sms, base), units / (4 * wlq::DEC_WARPS))
+                                         : std::min(4ll * sms / base, units / (2 * wlq::DEC_WARPS));
+        p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, 128)));
     }
     if (p.splits > 1) {
         const size_t parts = static_cast<size_t>(tokens) * q_heads * p.splits;
@@ -165,9 +168,9 @@ wlq_status launch_attention(const wlq::AttnArgs& a, const DecPlan& p, DeviceInfo
         e = p.nt == 1 ? launch_dec<D, 1, 1>(gx, s, a, d) : launch_dec<D, 2, 1>(gx, s, a, d);
     }
     if (e == cudaSuccess && p.splits > 1) {
-        const int64_t units = cdiv(static_cast<int64_t>(a.B.batch) * a.B.max_q * a.q_heads, 8);
+        const int64_t units = static_cast<int64_t>(a.B.batch) * a.B.max_q * a.q_heads;
         if (units >= (int64_t(1) << 31)) return fail(WLQ_ERR_SHAPE, "too many queries in one call");
-        e = launch_k(wlq::kv4_combine_kernel<D>, static_cast<unsigned>(units), 256, 0, s, a);
+        e = launch_k(wlq::kv4_combine_kernel<D>, static_cast<unsigned>(units), 128, 0, s, a);
     }
     return e == cudaSuccess ? WLQ_OK : cuda_fail(e, "kv4_attention launch");
 }

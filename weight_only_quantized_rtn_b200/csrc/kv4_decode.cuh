@@ -163,48 +163,67 @@ __device__ __forceinline__ void dec_pages(const AttnArgs& a, const int32_t* tabl
     }
 }
 
-// A unit's codes and scales on their way into a stage.
+// What a lane needs to fetch units: its pieces of the pool's first page of this
+// head, and how far a page and a token are.
 template <int D, int G>
-__device__ __forceinline__ void dec_fetch(const AttnArgs& a, int h, int unit, const uint32_t (&pg)[2], int lane, uint32_t stage) {
+struct DecFetch {
     using R = DecRing<D, G>;
-    constexpr int CPR = D / 32;      // pieces of a row
-    constexpr int RPI = 32 / CPR;    // rows of one instruction
-    const uint32_t npages = static_cast<uint32_t>(a.P.pages);
-    int64_t row[2];
+    static constexpr int CPR = D / 32;    // pieces of a row
+    static constexpr int RPI = 32 / CPR;  // rows of one instruction
+    const uint8_t *k, *v, *sc;
+    uint32_t page_codes, page_scales, npages, pmask;
+    uint32_t dst, dst_sc;  // places in a stage
+    int sc_tile;           // whose scales this lane fetches (-1: none)
+    __device__ __forceinline__ DecFetch(const AttnArgs& a, int h, int lane) {
+        const int r0 = lane / CPR, c = lane % CPR;
+        const int64_t head = static_cast<int64_t>(h) << a.P.page_shift;
+        k = a.P.k + (head + r0) * R::ROW + c * 16;
+        v = a.P.v + (head + r0) * R::ROW + c * 16;
+        page_codes = static_cast<uint32_t>(a.P.heads << a.P.page_shift) * R::ROW;  // at most 2^30
+        page_scales = static_cast<uint32_t>(a.P.heads << a.P.page_shift) * (2 * G);
+        npages = static_cast<uint32_t>(a.P.pages);
+        pmask = (1u << a.P.page_shift) - 1;
+        dst = R::at(r0, c);  // eight rows further the piece's place is the same
+        const int which = lane / (4 * G), idx = lane % (4 * G), off = idx % (2 * G);
+        sc_tile = lane < 8 * G ? idx / (2 * G) : -1;
+        sc = reinterpret_cast<const uint8_t*>(which ? a.P.vs : a.P.ks) + head * (2 * G) + off * 16;
+        dst_sc = 2 * R::CODES + which * R::SCALES + idx * 16;
+    }
+    // A unit's codes and scales on their way into a stage.
+    __device__ __forceinline__ void operator()(int unit, const uint32_t (&pg)[2], uint32_t stage) const {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-        row[t] = ((static_cast<int64_t>(pg[t]) * a.P.heads + h) << a.P.page_shift) + ((unit * DEC_UNIT + 16 * t) & ((1 << a.P.page_shift) - 1));
-    const int c = lane % CPR, r0 = lane / CPR;
+        for (int t = 0; t < 2; ++t) {
+            if (pg[t] < npages) {
+                const uint32_t place = static_cast<uint32_t>(unit * DEC_UNIT + 16 * t) & pmask;
+                const uint64_t at = static_cast<uint64_t>(pg[t]) * page_codes + place * R::ROW;
+                const uint8_t *kp = k + at, *vp = v + at;
+                const uint32_t d = stage + dst + 16 * t * R::ROW;
 #pragma unroll
-    for (int i = 0; i < DEC_UNIT / RPI; ++i) {
-        const int r = r0 + i * RPI, t = (i * RPI) >> 4;  // an instruction's rows lie in one tile
-        if (pg[t] < npages) {
-            const int64_t at = (row[t] + (r & 15)) * R::ROW + c * 16;
-            cp_async16(stage + R::at(r, c), a.P.k + at);
-            cp_async16(stage + R::CODES + R::at(r, c), a.P.v + at);
+                for (int i = 0; i < 16 / RPI; ++i) {
+                    cp_async16(d + i * RPI * R::ROW, kp + i * RPI * R::ROW);
+                    cp_async16(d + R::CODES + i * RPI * R::ROW, vp + i * RPI * R::ROW);
+                }
+                if (sc_tile == t) cp_async16(stage + dst_sc, sc + static_cast<uint64_t>(pg[t]) * page_scales + place * (2 * G));
+            }
         }
     }
-    if (lane < 8 * G) {
-        const int which = lane / (4 * G), idx = lane % (4 * G), t = idx / (2 * G), off = idx % (2 * G);
-        if ((t ? pg[1] : pg[0]) < npages)
-            cp_async16(stage + 2 * R::CODES + which * R::SCALES + idx * 16,
-                       reinterpret_cast<const uint8_t*>((which ? a.P.vs : a.P.ks) + (t ? row[1] : row[0]) * G) + off * 16);
-    }
-}
+};
 
-// G fp16 scales of one token.
+// G fp16 scales of one token, two a word (G == 1: one, the other half 0).
 template <int G>
-__device__ __forceinline__ void load_scales(const uint8_t* p, __half (&s)[G]) {
+__device__ __forceinline__ void load_scales(const uint8_t* p, uint32_t (&s)[(G + 1) / 2]) {
     if constexpr (G == 1) {
-        s[0] = *reinterpret_cast<const __half*>(p);
+        s[0] = *reinterpret_cast<const uint16_t*>(p);
     } else if constexpr (G == 2) {
-        const __half2 x = *reinterpret_cast<const __half2*>(p);
-        s[0] = __low2half(x); s[1] = __high2half(x);
+        s[0] = *reinterpret_cast<const uint32_t*>(p);
     } else {
         const uint2 u = *reinterpret_cast<const uint2*>(p);
-        s[0] = __low2half(bits_h2(u.x)); s[1] = __high2half(bits_h2(u.x));
-        s[2] = __low2half(bits_h2(u.y)); s[3] = __high2half(bits_h2(u.y));
+        s[0] = u.x;
+        s[1] = u.y;
     }
+}
+__device__ __forceinline__ float scale_of(const uint32_t* s, int i) {
+    return __half2float((i & 1) ? __high2half(bits_h2(s[i / 2])) : __low2half(bits_h2(s[i / 2])));
 }
 
 template <int D, int NT, int G>
@@ -242,13 +261,13 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
     // the first units on their way
     const uint32_t ring = smem_u32(dec_smem) + warp * DEC_STAGES * R::STAGE;
     const int32_t* table = a.B.table + b * a.B.table_stride;
-    const uint32_t npages = static_cast<uint32_t>(a.P.pages);
+    const DecFetch<D, G> fetch(a, h, lane);
     uint32_t pg[DEC_STAGES][2];  // pages of the units in flight, in order
 #pragma unroll
     for (int i = 0; i < DEC_STAGES; ++i) dec_pages(a, table, ub + warp + i * DEC_WARPS, ue, hi, pg[i]);
 #pragma unroll
     for (int i = 0; i < DEC_STAGES - 1; ++i) {
-        dec_fetch<D, G>(a, h, ub + warp + i * DEC_WARPS, pg[i], lane, ring + i * R::STAGE);
+        fetch(ub + warp + i * DEC_WARPS, pg[i], ring + i * R::STAGE);
         cp_async_commit();
     }
 
@@ -316,7 +335,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
         // the unit two ahead, into the stage read last
         {
             const int ahead = u + (DEC_STAGES - 1) * DEC_WARPS, st = stage == 0 ? DEC_STAGES - 1 : stage - 1;
-            if (ahead < ue) dec_fetch<D, G>(a, h, ahead, pg[DEC_STAGES - 1], lane, ring + st * R::STAGE);
+            if (ahead < ue) fetch(ahead, pg[DEC_STAGES - 1], ring + st * R::STAGE);
             cp_async_commit();
         }
         cp_async_wait<DEC_STAGES - 1>();
@@ -324,12 +343,11 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
         const uint32_t sk = ring + stage * R::STAGE, sv = sk + R::CODES;
         const uint8_t* sc = dec_smem + (sk - smem_u32(dec_smem)) + 2 * R::CODES;
         const int tok0 = u * DEC_UNIT;
-        const bool in0 = pg[0][0] < npages, in1 = pg[0][1] < npages;
+        const bool in0 = pg[0][0] < fetch.npages, in1 = pg[0][1] < fetch.npages;
         const bool inside = tok0 >= lo_all && tok0 + DEC_UNIT <= hi_all && in0 && in1;
         if (!inside && ((!in0 && tok0 < hi) || (!in1 && tok0 + 16 < hi)) && lane == 0) raise_error(ERRBIT_INDEX);
         float x[2][NT][4];
-        __half vs[2][2][G];
-        uint32_t vmax = 0;
+        uint32_t vs[2][2][(G + 1) / 2];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
             float acc[NT][G][4];
@@ -365,26 +383,19 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
                     mma16816_f16(acc[nt][w / BPG], fa[2], fb[2], fa[3], fb[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
                 }
             }
-            __half ks[2][G];
+            uint32_t ks[2][(G + 1) / 2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int tk = 16 * mt + 8 * r + g;
-                load_scales<G>(sc + tk * G * 2, ks[r]);
-                load_scales<G>(sc + R::SCALES + tk * G * 2, vs[mt][r]);
-                const bool there = inside || (tok0 + tk < kv && (mt ? in1 : in0));  // places no token was written to may hold anything
-#pragma unroll
-                for (int i = 0; i < G; ++i) {
-                    if (!there) vs[mt][r][i] = __ushort_as_half(0);
-                    vmax = max(vmax, static_cast<uint32_t>(__half_as_ushort(vs[mt][r][i])));
-                }
+                load_scales<G>(sc + (16 * mt + 8 * r + g) * G * 2, ks[r]);
+                load_scales<G>(sc + R::SCALES + (16 * mt + 8 * r + g) * G * 2, vs[mt][r]);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    float s = acc[nt][0][k] * __half2float(ks[k >> 1][0]);
+                    float s = acc[nt][0][k] * scale_of(ks[k >> 1], 0);
 #pragma unroll
-                    for (int i = 1; i < G; ++i) s = fmaf(acc[nt][i][k], __half2float(ks[k >> 1][i]), s);
+                    for (int i = 1; i < G; ++i) s = fmaf(acc[nt][i][k], scale_of(ks[k >> 1], i), s);
                     x[mt][nt][k] = s * cs[nt][k & 1];
                 }
         }
@@ -398,7 +409,20 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
                         const int tok = tok0 + 16 * mt + 8 * (k >> 1) + g;
                         if (tok < clo[nt][k & 1] || tok >= chi[nt][k & 1] || !(mt ? in1 : in0)) x[mt][nt][k] = -INFINITY;
                     }
+            // places no token was written to may hold anything
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    if (tok0 + 16 * mt + 8 * r + g >= kv || !(mt ? in1 : in0))
+#pragma unroll
+                        for (int i = 0; i < (G + 1) / 2; ++i) vs[mt][r][i] = 0;
         }
+        __half2 vm2 = bits_h2(0u);
+#pragma unroll
+        for (int i = 0; i < (G + 1) / 2; ++i)
+            vm2 = __hmax2(vm2, __hmax2(__hmax2(bits_h2(vs[0][0][i]), bits_h2(vs[0][1][i])), __hmax2(bits_h2(vs[1][0][i]), bits_h2(vs[1][1][i]))));
+        uint32_t vmax = max(h2_bits(vm2) & 0xFFFFu, h2_bits(vm2) >> 16);
         bool move = vmax > vtop;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -449,7 +473,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
                     l[nt][1] += p1;
 #pragma unroll
                     for (int i = 0; i < G; ++i) {
-                        const float v = __half2float(vs[mt][r][i]);
+                        const float v = scale_of(vs[mt][r], i);
                         pf[mt][nt][i][r] = movmatrix(h2_bits(__floats2half2_rn(p0 * v, p1 * v)));
                     }
                 }
@@ -539,42 +563,51 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
     }
 }
 
-// Joins the splits' parts in order: one warp per query and head; grid (units of
-// 8 warps) over batch * max_q * q_heads.
+// Joins the splits' parts: a CTA of four warps per query and head (grid over
+// batch * max_q * q_heads), each warp a quarter of the splits in order, then
+// the four sums in order.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_combine_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(128) kv4_combine_kernel(const AttnArgs a) {
+    constexpr int V = D / 32;
+    __shared__ float sm[4][D + 1];
     grid_dependency_sync();
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int head = static_cast<int>(unit % a.q_heads);
-    const int64_t bi = unit / a.q_heads;
-    const int b = static_cast<int>(bi / a.B.max_q), i = static_cast<int>(bi % a.B.max_q);
-    if (b >= a.B.batch) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int head = blockIdx.x % a.q_heads, bi = blockIdx.x / a.q_heads;
+    const int b = bi / a.B.max_q, i = bi % a.B.max_q;
     const int64_t r0 = a.B.cu[b], r1 = a.B.cu[b + 1];
-    if (kv_sequence(r0, r1, a.B.kv_len[b], a.B.max_q, a.B.tokens) != KV_OK || i >= r1 - r0) return;
+    if (kv_sequence(r0, r1, a.B.kv_len[b], a.B.max_q, a.B.tokens) != KV_OK || i >= r1 - r0) return;  // the whole CTA
     const int64_t head_row = (r0 + i) * a.q_heads + head;
     const float2* ml = a.part_ml + head_row * a.splits;
     float M = -INFINITY;
     for (int s = lane; s < a.splits; s += 32) M = fmaxf(M, ml[s].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    constexpr int V = D / 32;
     float acc[V] = {}, L = 0.0f;
     const float* po = a.part_o + head_row * a.splits * D + lane * V;
-#pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
+#pragma unroll 8
+    for (int s = warp; s < a.splits; s += 4) {
         const float2 x = ml[s];
         const float w = M == -INFINITY ? 0.0f : ex2(x.x - M);
         L += w * x.y;
-#pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] += w * po[static_cast<int64_t>(s) * D + k];
+        if constexpr (V == 4) {
+            const float4 o = *reinterpret_cast<const float4*>(po + static_cast<int64_t>(s) * D);
+            acc[0] += w * o.x; acc[1] += w * o.y; acc[2] += w * o.z; acc[3] += w * o.w;
+        } else {
+            const float2 o = *reinterpret_cast<const float2*>(po + static_cast<int64_t>(s) * D);
+            acc[0] += w * o.x; acc[1] += w * o.y;
+        }
     }
-    const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
-    uint16_t* out = a.out + head_row * D + lane * V;
 #pragma unroll
-    for (int k = 0; k < V; k += 2)
-        *reinterpret_cast<__nv_bfloat162*>(out + k) = __floats2bfloat162_rn(acc[k] * inv, acc[k + 1] * inv);
-    if (a.lse && lane == 0) a.lse[head_row] = L > 0.0f ? (M + __log2f(L)) * 0.6931471805599453f : (L == 0.0f ? -INFINITY : L);
+    for (int k = 0; k < V; ++k) sm[warp][lane * V + k] = acc[k];
+    if (lane == 0) sm[warp][D] = L;
+    __syncthreads();
+    L = (sm[0][D] + sm[1][D]) + (sm[2][D] + sm[3][D]);
+    const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
+    for (int d = 2 * static_cast<int>(threadIdx.x); d < D; d += 256) {
+        const float x = (sm[0][d] + sm[1][d]) + (sm[2][d] + sm[3][d]), y = (sm[0][d + 1] + sm[1][d + 1]) + (sm[2][d + 1] + sm[3][d + 1]);
+        *reinterpret_cast<__nv_bfloat162*>(a.out + head_row * D + d) = __floats2bfloat162_rn(x * inv, y * inv);
+    }
+    if (a.lse && threadIdx.x == 0) a.lse[head_row] = L > 0.0f ? (M + __log2f(L)) * 0.6931471805599453f : (L == 0.0f ? -INFINITY : L);
 }
 
 }  // namespace wlq

@@ -42,7 +42,7 @@ namespace wlq {
 
 constexpr int ROPE_MAX_AXES = 4;
 constexpr int ROPE_MAX_PAIRS = 64;
-constexpr int KV_THREADS = 256;
+constexpr int KV_THREADS = 128;
 // 4-bit cache rows hold values up to this magnitude: with a scale of
 // fp16(a / 7) every code times its scale stays finite in fp16.
 constexpr float KV4_MAX_ABS = 65280.0f;  // the largest bf16 below 2^16
@@ -93,13 +93,10 @@ struct KvBatch {
     int64_t tokens;  // rows of the token-indexed tensors
 };
 
-__device__ __forceinline__ void unpack8(uint4 u, float (&f)[8]) {
+__device__ __forceinline__ void unpack8(uint4 u, float2 (&f)[4]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
 __device__ __forceinline__ uint32_t bf16_rn_bits(float y) {
@@ -177,68 +174,87 @@ struct RopeLane {
 
 // One row: x (8 bf16 values a lane) to the rounded bits, two per word.
 template <int D, bool INTER>
-__device__ __forceinline__ uint4 norm_rope_row(uint4 raw, const float (&w)[8], bool norm, bool rope, const RopeArgs& a,
+__device__ __forceinline__ uint4 norm_rope_row(uint4 raw, const float2 (&w)[4], bool norm, bool rope, const RopeArgs& a,
                                                const RopeLane<D, INTER>& R, const TokenTurns& T) {
-    constexpr int LPR = D / 8;
+    constexpr int LPR = D / 8, RM = INTER ? 3 : 7;
     if (!norm && !rope) return raw;
-    float x[8];
+    float2 x[4];
     unpack8(raw, x);
     float r = 1.0f;
     if (norm) {
-        const float s01 = __fadd_rn(x[0] * x[0], x[1] * x[1]), s23 = __fadd_rn(x[2] * x[2], x[3] * x[3]);
-        const float s45 = __fadd_rn(x[4] * x[4], x[5] * x[5]), s67 = __fadd_rn(x[6] * x[6], x[7] * x[7]);
-        float ss = (s01 + s23) + (s45 + s67);
+        const float2 q = add_f32x2(add_f32x2(mul_f32x2(x[0], x[0]), mul_f32x2(x[1], x[1])),
+                                   add_f32x2(mul_f32x2(x[2], x[2]), mul_f32x2(x[3], x[3])));
+        float ss = q.x + q.y;
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         r = __frsqrt_rn(fmaf(ss, 1.0f / D, static_cast<float>(a.eps)));
     }
-    float p[8], y[8], gap = INFINITY;  // the least distance of a bf16 midpoint beyond E
+    float2 p[4], y[4], d[4];
+    float e[4];
     const float k = r * 5.364418029785156e-7f;  // 9 * 2^-24 r
+    const float2 r2 = make_float2(r, r);
+    bool near = false;  // a bf16 midpoint lies within E
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= w[i];  // exact: 8 x 8 bits
+    for (int i = 0; i < 4; ++i) x[i] = mul_f32x2(x[i], w[i]);  // exact: 8 x 8 bits
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if constexpr (INTER) p[i] = (i & 1) ? x[i - 1] : -x[i + 1];
-        else p[i] = __shfl_sync(0xffffffffu, x[i], R.src);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float c = INTER ? R.c[i / 2] : R.c[i % (INTER ? 4 : 8)], s = INTER ? R.s[i / 2] : R.s[i % (INTER ? 4 : 8)];
-        y[i] = fmaf(x[i], c, p[i] * s) * r;
-        const float mid = __uint_as_float((__float_as_uint(y[i]) & 0xFFFF0000u) | 0x8000u);
-        gap = fminf(gap, fmaf(fabsf(x[i]) + fabsf(p[i]), -k, fabsf(y[i] - mid)));
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (INTER) p[i] = make_float2(-x[i].y, x[i].x);
+        else p[i] = make_float2(__shfl_sync(0xffffffffu, x[i].x, R.src), __shfl_sync(0xffffffffu, x[i].y, R.src));
     }
     uint4 out;
     uint32_t* o = reinterpret_cast<uint32_t*>(&out);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+        const float2 c = INTER ? make_float2(R.c[i], R.c[i]) : make_float2(R.c[(2 * i) & RM], R.c[(2 * i + 1) & RM]);
+        const float2 s = INTER ? make_float2(R.s[i], R.s[i]) : make_float2(R.s[(2 * i) & RM], R.s[(2 * i + 1) & RM]);
+        y[i] = mul_f32x2(fma_f32x2(x[i], c, mul_f32x2(p[i], s)), r2);
+        // minus the midpoint above: the upper half's bits, 0x8000 below, the sign turned
+        const float2 mid = make_float2(__uint_as_float((__float_as_uint(y[i].x) & 0xFFFF0000u) ^ 0x80008000u),
+                                       __uint_as_float((__float_as_uint(y[i].y) & 0xFFFF0000u) ^ 0x80008000u));
+        d[i] = add_f32x2(y[i], mid);
+        if constexpr (INTER) {
+            e[i] = (fabsf(x[i].x) + fabsf(x[i].y)) * k;
+            near |= fabsf(d[i].x) <= e[i];
+            near |= fabsf(d[i].y) <= e[i];
+        } else {
+            near |= fabsf(d[i].x) <= (fabsf(x[i].x) + fabsf(p[i].x)) * k;
+            near |= fabsf(d[i].y) <= (fabsf(x[i].y) + fabsf(p[i].y)) * k;
+        }
+        const __nv_bfloat162 b = __floats2bfloat162_rn(y[i].x, y[i].y);
         o[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    if (__any_sync(0xffffffffu, gap <= 0.0f)) {
+    if (__any_sync(0xffffffffu, near)) {
         double r64 = 1.0;
         if (norm) {
             double ss = 0.0;
-            float f[8];
+            float2 f[4];
             unpack8(raw, f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fma(static_cast<double>(f[i]), static_cast<double>(f[i]), ss);
+            for (int i = 0; i < 4; ++i) {
+                ss = fma(static_cast<double>(f[i].x), static_cast<double>(f[i].x), ss);
+                ss = fma(static_cast<double>(f[i].y), static_cast<double>(f[i].y), ss);
+            }
 #pragma unroll
             for (int j = LPR / 2; j > 0; j >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, j);
-            r64 = 1.0 / sqrt(ss / D + a.eps);
+            // two Newton steps from the fp32 root: 2^-22 -> 2^-43 -> fp64's own rounding
+            const double v = 0.5 * (ss / D + a.eps);
+            r64 = static_cast<double>(r);
+            r64 = r64 * fma(-v * r64, r64, 1.5);
+            r64 = r64 * fma(-v * r64, r64, 1.5);
         }
-        if (gap <= 0.0f) {
+        if (near) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float mid = __uint_as_float((__float_as_uint(y[i]) & 0xFFFF0000u) | 0x8000u);
-                if (fmaf(fabsf(x[i]) + fabsf(p[i]), -k, fabsf(y[i] - mid)) > 0.0f) continue;
+                const float xi = (i & 1) ? x[i / 2].y : x[i / 2].x, pi = (i & 1) ? p[i / 2].y : p[i / 2].x;
+                const float di = (i & 1) ? d[i / 2].y : d[i / 2].x;
+                if (!(fabsf(di) <= (fabsf(xi) + fabsf(pi)) * k)) continue;
                 double c = 1.0, s = 0.0;
                 if (R.first >= 0) {
                     const double2 t = T.d[R.first + (INTER ? i / 2 : i)];
                     c = t.x;
                     s = R.lo ? -t.y : t.y;
                 }
-                const uint32_t b = bf16_from_f64((static_cast<double>(x[i]) * c + static_cast<double>(p[i]) * s) * r64);
+                const uint32_t b = bf16_from_f64((static_cast<double>(xi) * c + static_cast<double>(pi) * s) * r64);
                 o[i / 2] = (i & 1) ? ((o[i / 2] & 0xFFFFu) | (b << 16)) : ((o[i / 2] & 0xFFFF0000u) | b);
             }
         }
@@ -247,14 +263,12 @@ __device__ __forceinline__ uint4 norm_rope_row(uint4 raw, const float (&w)[8], b
     return out;
 }
 
-__device__ __forceinline__ void load_weight8(const uint16_t* w, int l, float (&f)[8]) {
-    if (w) {
+__device__ __forceinline__ void load_weight8(const uint16_t* w, int l, float2 (&f)[4]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(static_cast<uint32_t>(__ldg(w + 8 * l + i)) << 16);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = 1.0f;
-    }
+    for (int i = 0; i < 4; ++i)
+        f[i] = w ? make_float2(__uint_as_float(static_cast<uint32_t>(__ldg(w + 8 * l + 2 * i)) << 16),
+                               __uint_as_float(static_cast<uint32_t>(__ldg(w + 8 * l + 2 * i + 1)) << 16))
+                 : make_float2(1.0f, 1.0f);
 }
 
 // grid (tokens, splits of the token's rows); a CTA takes rows y, y + splits, ...
@@ -283,7 +297,7 @@ __global__ void __launch_bounds__(KV_THREADS) qk_norm_rope_kernel(const HeadRows
     __syncthreads();
     RopeLane<D, INTER> R;
     R.load(a, turns, rope, lane);
-    float w[8];
+    float2 w[4];
     int held = -1;  // whose weight w holds
     for (; b < bites; b += step) {
         const uint4 next = fetch(b + step);
@@ -327,11 +341,47 @@ __device__ __forceinline__ int64_t kv_row(const Kv4Pool& P, const KvSlot& s, int
     return ((s.page * P.heads + h) << P.page_shift) + s.place;
 }
 
-// 8 codes (bytes, two's complement, two words) as one word of the cache.
-__device__ __forceinline__ uint32_t kv4_word(uint32_t c0, uint32_t c1) {
-    c0 = __vadd4(c0, 0x08080808u);
-    c1 = __vadd4(c1, 0x08080808u);
-    return __byte_perm(c0 | (c0 >> 12), c1 | (c1 >> 12), 0x5140);
+// The scale fp16(a / 7) of a group, a the largest magnitude of bf16 values: the
+// fp32 quotient, rounded to nearest (one Newton step on a / 7 with the exact
+// remainder), rounds to the fp16 value nearest to the real quotient.  A
+// midpoint m of two fp16 values has at most 12 bits; if 7 m is not a, which has
+// 8, the two differ by 2^-15 of their size at least, far more than the fp32
+// rounding; if it is, the quotient is exact.
+__device__ __forceinline__ float kv4_scale(float a) {
+    const float q = a * 0.14285714924335480f;
+    return __half2float(__float2half_rn(fmaf(fmaf(-7.0f, q, a), 0.14285714924335480f, q)));
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 8 bf16 values of a group with scale s > 0 as a word of the cache.
+// code = the integer nearest to x / s, ties to even, exactly: x has 8
+// significant bits and s at most 11, so x / s is a half-integer or at least
+// 2^-12 away from one.  x * inv (2^-20 off at most) is first rounded to a
+// multiple of 2^-14 -- a half-integer if and only if the quotient is one -- by
+// the fma's addition of 1.5 * 2^9, then to an integer, ties to even, by the
+// step to 1.5 * 2^23 + 8, which leaves code + 8 in the low bits.
+// |x / s| is below 7.5 unless s is an fp16 subnormal (its rounding may be
+// half of it): then the sums are clamped.
+__device__ __forceinline__ uint32_t kv4_quantize(const float2 (&x)[4], float s) {
+    const float inv = rcp_approx(s);
+    const float2 inv2 = make_float2(inv, inv), m1 = make_float2(768.0f, 768.0f), m2 = make_float2(12582920.0f - 768.0f, 12582920.0f - 768.0f);
+    float2 u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = add_f32x2(fma_f32x2(x[i], inv2, m1), m2);
+    if (s < 6.103515625e-5f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            u[i] = make_float2(fminf(fmaxf(u[i].x, 12582913.0f), 12582927.0f), fminf(fmaxf(u[i].y, 12582913.0f), 12582927.0f));
+    }
+    // inputs 0, 4, 1, 5 at the bytes' low nibbles, 2, 6, 3, 7 at the high ones
+    const uint32_t lo = __byte_perm(__byte_perm(__float_as_uint(u[0].x), __float_as_uint(u[2].x), 0x0040),
+                                    __byte_perm(__float_as_uint(u[0].y), __float_as_uint(u[2].y), 0x0040), 0x5410);
+    const uint32_t hi = __byte_perm(__byte_perm(__float_as_uint(u[1].x), __float_as_uint(u[3].x), 0x0040),
+                                    __byte_perm(__float_as_uint(u[1].y), __float_as_uint(u[3].y), 0x0040), 0x5410);
+    return lo | (hi << 4);
 }
 
 // grid (max_q * batch, splits of the token's 2 H rows): key rows, then value
@@ -359,7 +409,7 @@ __global__ void __launch_bounds__(KV_THREADS) kv4_append_kernel(const HeadRows k
     int t = blockIdx.y * (KV_THREADS / 32) + warp;
     uint4 next = fetch(t);
     if (rope) token_turns(a, slot.row, turns);
-    float w[8];
+    float2 w[4];
     load_weight8(k.w, l, w);
     __syncthreads();
     RopeLane<D, INTER> R;
@@ -379,19 +429,17 @@ __global__ void __launch_bounds__(KV_THREADS) kv4_append_kernel(const HeadRows k
         for (int o = (1 << lg8) >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float amax = __uint_as_float(m << 16);
         const bool gbad = !(amax <= KV4_MAX_ABS);  // too large, an infinity or a NaN
-        const float s = gbad ? 0.0f : stored_scale<SCALE_F16>(amax, 7);
+        const float s = gbad ? 0.0f : kv4_scale(amax);
         bad |= gbad && in;
-        uint32_t c0 = 0, c1 = 0;
+        uint32_t word = 0x88888888u;
         if (s > 0.0f) {
-            float f[8];
+            float2 f[4];
             unpack8(raw, f);
-            const float inv = __frcp_rn(s);
-            c0 = rtn4_f32_clamped(make_float4(f[0], f[1], f[2], f[3]), s, inv, 0.5f * s, 7.0f);
-            c1 = rtn4_f32_clamped(make_float4(f[4], f[5], f[6], f[7]), s, inv, 0.5f * s, 7.0f);
+            word = kv4_quantize(f, s);
         }
         if (in) {
             const int64_t row = kv_row(P, slot, h);
-            reinterpret_cast<uint32_t*>(isk ? P.k : P.v)[row * LPR + l] = kv4_word(c0, c1);
+            reinterpret_cast<uint32_t*>(isk ? P.k : P.v)[row * LPR + l] = word;
             if ((l & ((1 << lg8) - 1)) == 0)
                 (isk ? P.ks : P.vs)[row * (LPR >> lg8) + (l >> lg8)] = __float2half_rn(s);
         }
@@ -399,15 +447,18 @@ __global__ void __launch_bounds__(KV_THREADS) kv4_append_kernel(const HeadRows k
     if (bad) raise_error(ERRBIT_NONFINITE);
 }
 
-// Two bf16 values code * scale (one rounding) of nibble pairs of a word.
+// Eight bf16 values code * scale (one rounding) of a word: codes as fp32 by
+// 2^23 + u - (2^23 + 8).
 __device__ __forceinline__ uint4 kv4_values(uint32_t word, float s) {
     uint4 out;
     uint32_t* o = reinterpret_cast<uint32_t*>(&out);
+    const float2 off = make_float2(-8388616.0f, -8388616.0f), s2 = make_float2(s, s);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {  // inputs 2 j (nibble j) and 2 j + 1 (nibble 4 + j)
-        const float lo = static_cast<float>(static_cast<int>(word >> (4 * j) & 15u) - 8) * s;
-        const float hi = static_cast<float>(static_cast<int>(word >> (16 + 4 * j) & 15u) - 8) * s;
-        const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+        const uint32_t v = word >> (4 * j);
+        const float2 u = make_float2(__uint_as_float((v & 15u) | 0x4B000000u), __uint_as_float((v >> 16 & 15u) | 0x4B000000u));
+        const float2 y = mul_f32x2(add_f32x2(u, off), s2);
+        const __nv_bfloat162 p = __floats2bfloat162_rn(y.x, y.y);
         o[j] = *reinterpret_cast<const uint32_t*>(&p);
     }
     return out;
