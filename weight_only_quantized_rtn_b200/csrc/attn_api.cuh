@@ -122,8 +122,8 @@ DecPlan dec_plan(int64_t tokens, int batch, int max_q, int64_t max_kv, int q_hea
         // Many sequences: about three rounds of four CTAs an SM, so that ragged ones even out, with at least four
         // units for each warp of a part.  Few: one round (37 parts a head against 111 took 85 us against 100 for two
         // sequences of up to 131072 tokens), with two units for each warp.
-        const int64_t want = base >= sms ? std::min(cdiv(12ll * sms, base), units / (4 * wlq::DEC_WARPS))
-                                         : std::min(4ll * sms / base, units / (2 * wlq::DEC_WARPS));
+        const int64_t want = base >= sms ? std::min<int64_t>(cdiv(12ll * sms, base), units / (4 * wlq::DEC_WARPS))
+                                         : std::min<int64_t>(4ll * sms / base, units / (2 * wlq::DEC_WARPS));
         p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, 128)));
     }
     if (p.splits > 1) {
