@@ -66,14 +66,20 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 
+// (w & mask) | 0x64006400 in one instruction (as C it becomes two, each with an immediate).
+__device__ __forceinline__ __half2 magic_pair(uint32_t w, uint32_t mask) {
+    uint32_t o;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(o) : "r"(w), "r"(mask), "r"(0x64006400u));
+    return bits_h2(o);
+}
 // Four pairs of nibbles of w (nibble i of each half, i = 0..3) as fp16 code * s.
 __device__ __forceinline__ void nibbles_f16(uint32_t w, __half2 s, uint32_t (&o)[4]) {
     const __half2 k1032 = bits_h2(0x64086408u), k16 = bits_h2(0x2C002C00u), k72 = bits_h2(0xD480D480u);  // 1032, 1/16, -72
     const uint32_t v = w >> 8;
-    o[0] = h2_bits(__hmul2(__hsub2(bits_h2((w & 0x000F000Fu) | 0x64006400u), k1032), s));
-    o[1] = h2_bits(__hmul2(__hfma2(bits_h2((w & 0x00F000F0u) | 0x64006400u), k16, k72), s));
-    o[2] = h2_bits(__hmul2(__hsub2(bits_h2((v & 0x000F000Fu) | 0x64006400u), k1032), s));
-    o[3] = h2_bits(__hmul2(__hfma2(bits_h2((v & 0x00F000F0u) | 0x64006400u), k16, k72), s));
+    o[0] = h2_bits(__hmul2(__hsub2(magic_pair(w, 0x000F000Fu), k1032), s));
+    o[1] = h2_bits(__hmul2(__hfma2(magic_pair(w, 0x00F000F0u), k16, k72), s));
+    o[2] = h2_bits(__hmul2(__hsub2(magic_pair(v, 0x000F000Fu), k1032), s));
+    o[3] = h2_bits(__hmul2(__hfma2(magic_pair(v, 0x00F000F0u), k16, k72), s));
 }
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
@@ -126,10 +132,10 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
 __device__ __forceinline__ void nibbles_codes(uint32_t w, uint32_t (&o)[4]) {
     const __half2 k1032 = bits_h2(0x64086408u), k16 = bits_h2(0x2C002C00u), k72 = bits_h2(0xD480D480u);  // 1032, 1/16, -72
     const uint32_t v = w >> 8;
-    o[0] = h2_bits(__hsub2(bits_h2((w & 0x000F000Fu) | 0x64006400u), k1032));
-    o[1] = h2_bits(__hfma2(bits_h2((w & 0x00F000F0u) | 0x64006400u), k16, k72));
-    o[2] = h2_bits(__hsub2(bits_h2((v & 0x000F000Fu) | 0x64006400u), k1032));
-    o[3] = h2_bits(__hfma2(bits_h2((v & 0x00F000F0u) | 0x64006400u), k16, k72));
+    o[0] = h2_bits(__hsub2(magic_pair(w, 0x000F000Fu), k1032));
+    o[1] = h2_bits(__hfma2(magic_pair(w, 0x00F000F0u), k16, k72));
+    o[2] = h2_bits(__hsub2(magic_pair(v, 0x000F000Fu), k1032));
+    o[3] = h2_bits(__hfma2(magic_pair(v, 0x00F000F0u), k16, k72));
 }
 
 constexpr int DEC_STAGES = 3;
