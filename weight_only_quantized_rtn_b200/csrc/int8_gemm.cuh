@@ -60,21 +60,29 @@ __host__ __device__ constexpr uint32_t idesc_i8(uint32_t m, uint32_t n) {
            | (1u << 10)        // B s8
            | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
+constexpr uint32_t I8_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);  // descriptors' high word, as smem_desc_sw128
+// Issued by a converged warp (elect_one), descriptors given by their low words.
 template <bool PAIR>
-__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_i8(uint32_t on, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
     if constexpr (PAIR)
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+            "mov.b64 a, {%1, %5};\n\t"
+            "mov.b64 b, {%2, %5};\n\t"
             "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            "setp.ne.b32 q, %6, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::i8 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(I8_DESC_HI), "r"(on)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+            "mov.b64 a, {%1, %5};\n\t"
+            "mov.b64 b, {%2, %5};\n\t"
             "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            "setp.ne.b32 q, %6, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::i8 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(I8_DESC_HI), "r"(on)
             : "memory");
 }
 // A tile into this CTA's shared memory, completing on a barrier of the pair's
@@ -179,37 +187,42 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && (!PAIR || rank == 0)) {
+        if (!PAIR || rank == 0) {
             const uint32_t idesc = idesc_i8(PAIR ? 256 : 128, static_cast<uint32_t>(a.bn));
-            uint32_t it = 0, tc = 0;
+            const uint32_t on = elect_one();
+            const uint32_t lo0 = ((smem_u32(base) & 0x3FFFFu) >> 4) | (1u << 16);
+            uint32_t st = 0, ph = 0, tc = 0;
             for (int tile = first_tile; tile < a.tiles; tile += tile_step, ++tc) {
                 const uint32_t buf = tc & 1;
-                if (!nv_wait(&accempty[buf], ((tc >> 1) & 1) ^ 1, a.timeout_ns, abort_flag)) break;
+                if (!warp_wait(&accempty[buf], ((tc >> 1) & 1) ^ 1, a.timeout_ns, abort_flag)) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + buf * a.acc2;
                 bool ok = true;
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const uint32_t st = it % a.stages, ph = (it / a.stages) & 1;
-                    if (!nv_wait(&full[st], ph, a.timeout_ns, abort_flag)) { ok = false; break; }
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!warp_wait(&full[st], ph, a.timeout_ns, abort_flag)) { ok = false; break; }
                     tc_fence_after();
-                    const uint8_t* sb = base + static_cast<size_t>(st) * a.stage_bytes;
-                    const uint64_t da = smem_desc_sw128(smem_u32(sb)), db = smem_desc_sw128(smem_u32(sb + I8_A_BYTES));
+                    const uint32_t da = lo0 + st * (a.stage_bytes >> 4), db = da + (I8_A_BYTES >> 4);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_i8<PAIR>(acc, da + 2 * k, db + 2 * k, idesc, (kb > kb0 || k > 0) ? 1u : 0u);
-                    if constexpr (PAIR) mma_commit_pair_both(&empty[st], 0);
-                    else mma_commit(&empty[st]);
+                    for (int k = 0; k < 4; ++k) mma_i8<PAIR>(on, acc, da + 2 * k, db + 2 * k, idesc, static_cast<uint32_t>(kb - kb0) + k);
+                    if constexpr (PAIR) mma_commit_pair_both_on(on, &empty[st]);
+                    else mma_commit_on(on, &empty[st]);
+                    if (++st == static_cast<uint32_t>(a.stages)) {
+                        st = 0;
+                        ph ^= 1;
+                    }
                 }
                 if (!ok) break;
-                if constexpr (PAIR) mma_commit_pair_both(&accfull[buf], 0);
-                else mma_commit(&accfull[buf]);
+                if constexpr (PAIR) mma_commit_pair_both_on(on, &accfull[buf]);
+                else mma_commit_on(on, &accfull[buf]);
             }
-            // every MMA issued has completed before tensor memory is freed
-            if constexpr (PAIR) mma_commit_pair(drain);
-            else mma_commit(drain);
+            // every MMA issued has completed before tensor memory is freed (a pair's second CTA only sees its copy arrive)
+            if constexpr (PAIR) mma_commit_pair_both_on(on, drain);
+            else mma_commit_on(on, drain);
             const uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < a.timeout_ns) {
             }
         }
+        __syncwarp();
     } else {
         const int q = warp & 3;  // TMEM lane quarter this warp may read
         uint8_t* stg = epi_stage + static_cast<size_t>(warp - 2) * I8_EPI_STAGE;

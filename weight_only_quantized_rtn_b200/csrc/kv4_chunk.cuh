@@ -64,19 +64,8 @@ constexpr uint32_t CH_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo_k(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
 __device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr, uint32_t chunk) { return ((saddr & 0x3FFFFu) >> 4) | ((chunk >> 4) << 16); }
 
-// mma_ss / mma_ts / mma_commit issued by a whole converged warp, executed by its
-// lane with `on` set: addresses and descriptors (given by their low words) then
-// stay uniform values, which the instruction wants; from a divergent branch
-// every operand is moved there one by one, about twice the MMA's own 64 clocks.
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t on;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(on));
-    return on;
-}
+// mma_ss / mma_ts issued by a converged warp (ptx.cuh, elect_one), descriptors
+// given by their low words.
 __device__ __forceinline__ void mma_ss_lo(uint32_t on, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
@@ -98,15 +87,6 @@ __device__ __forceinline__ void mma_ts_lo(uint32_t on, uint32_t d_tmem, uint32_t
         "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(CH_DESC_HI), "r"(on)
         : "memory");
 }
-__device__ __forceinline__ void mma_commit_on(uint32_t on, uint64_t* bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-        "r"(on)
-        : "memory");
-}
-
 // Cached-token steps [jb, je) of a row tile within the CTA's split.
 struct ChRange {
     int jb, je;

@@ -168,6 +168,36 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
         : "memory");
 }
 
+// tcgen05 instructions issued by a whole converged warp and executed by its lane
+// with `on` set: addresses and descriptors then stay uniform values, which the
+// instruction wants; from a divergent branch (one lane's code) every operand is
+// moved there one by one, which takes about 100 clocks an MMA.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t on;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(on));
+    return on;
+}
+__device__ __forceinline__ void mma_commit_on(uint32_t on, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit_pair_both_on(uint32_t on, uint64_t* bar) {  // pair of cluster ranks 0 and 1
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3)), "r"(on)
+        : "memory");
+}
+
 // ------------------------------------------------- CTA-pair (cta_group::2)
 // Two CTAs of a cluster share one MMA: A rows 0-127 come from the first CTA's
 // TMEM, rows 128-255 from the second's; B columns are split between their
