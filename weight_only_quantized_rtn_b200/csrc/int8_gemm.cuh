@@ -155,27 +155,37 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
     const int kb1 = PAIR ? a.KB : static_cast<int>(static_cast<int64_t>(a.KB) * (rank + 1) / a.S);
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int tile = first_tile; tile < a.tiles && ok; tile += tile_step) {
-                const int nt = tile % a.NT, mt = tile / a.NT;
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const uint32_t st = it % a.stages, ph = (it / a.stages) & 1;
-                    if (!nv_wait(&empty[st], ph ^ 1, a.timeout_ns, abort_flag)) { ok = false; break; }
-                    uint8_t* sb = base + static_cast<size_t>(st) * a.stage_bytes;
+        // a converged warp, one lane of which issues the copies
+        const uint32_t on = elect_one();
+        uint32_t it = 0, st = 0, ph = 0;
+        bool ok = true;
+        const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
+        for (int tile = first_tile; tile < a.tiles && ok; tile += tile_step) {
+            const int nt = tile % a.NT, mt = tile / a.NT;
+            const int wrow = PAIR ? nt * 256 + static_cast<int>(rank) * 128 : nt * 128;
+            const int xrow = PAIR ? mt * a.bn + static_cast<int>(rank) * (a.bn / 2) : mt * a.bn;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                if (!warp_wait(&empty[st], ph ^ 1, a.timeout_ns, abort_flag)) { ok = false; break; }
+                uint8_t* sb = base + static_cast<size_t>(st) * a.stage_bytes;
+                if (on) {
                     if constexpr (PAIR) {
                         if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * a.stage_bytes);
-                        const uint32_t bar = mapa_shared(smem_u32(&full[st]), 0);
-                        tma_load_2d_pair(sb, &tm_w, bar, kb * 128, nt * 256 + static_cast<int>(rank) * 128);
-                        tma_load_2d_pair(sb + I8_A_BYTES, &tm_x, bar, kb * 128, mt * a.bn + static_cast<int>(rank) * (a.bn / 2));
+                        tma_load_2d_pair(sb, &tm_w, full0 + st * 8, kb * 128, wrow);
+                        tma_load_2d_pair(sb + I8_A_BYTES, &tm_x, full0 + st * 8, kb * 128, xrow);
                     } else {
                         mbar_arrive_expect_tx(&full[st], a.stage_bytes);
-                        tma_load_2d(sb, &tm_w, &full[st], kb * 128, nt * 128);
-                        tma_load_2d(sb + I8_A_BYTES, &tm_x, &full[st], kb * 128, mt * a.bn);
+                        tma_load_2d(sb, &tm_w, &full[st], kb * 128, wrow);
+                        tma_load_2d(sb + I8_A_BYTES, &tm_x, &full[st], kb * 128, xrow);
                     }
                 }
+                __syncwarp();
+                if (++st == static_cast<uint32_t>(a.stages)) {
+                    st = 0;
+                    ph ^= 1;
+                }
             }
+        }
+        if (lane == 0) {
             // copies still in flight land before the CTA leaves (bounded).  In a pair the first CTA's
             // barrier covers both; the second waits for its stages to be consumed instead.
             const uint32_t n = it < static_cast<uint32_t>(a.stages) ? it : static_cast<uint32_t>(a.stages);
