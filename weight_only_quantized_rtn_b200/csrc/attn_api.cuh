@@ -470,12 +470,12 @@ wlq_status int8_linear_impl(const void* xq, const float* xs, int64_t M, const vo
     a.tmem_cols = 2 * a.acc2;
     a.y_f32 = (y_dtype == WLQ_OUT_F32) ? 1 : 0;
     const size_t esize = a.y_f32 ? 4 : 2;
-    if (p.S == 1 && aligned16(y) && (static_cast<size_t>(N) * esize) % 16 == 0) {
+    if (p.S == 1 && p.bn % 32 == 0 && aligned16(y) && (static_cast<size_t>(N) * esize) % 16 == 0) {
         EncodeTiledFn fn = encode_fn();
         if (!fn) return fail(WLQ_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(N) * esize};
-        const cuuint32_t box[2] = {32, 16};
+        const cuuint32_t box[2] = {32, 32};
         const cuuint32_t estr[2] = {1, 1};
         const CUresult cr = fn(&ty, a.y_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, y, dims, strides, box,
                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,

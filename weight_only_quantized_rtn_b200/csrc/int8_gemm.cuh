@@ -19,7 +19,7 @@
 //    of a cluster when there are few tiles: the integer partial sums are added
 //    through distributed shared memory, in any order the same.
 // The accumulator is double-buffered, so a tile's epilogue runs under the next
-// tile's MMAs: 16 tokens x 32 channels at a time are scaled in fp32, staged
+// tile's MMAs: 32 tokens x 32 channels at a time are scaled in fp32, staged
 // and stored (TMA when y's rows are whole 16-byte units).
 #pragma once
 #include <cstdint>
@@ -33,7 +33,7 @@ namespace wlq {
 constexpr int I8_THREADS = 192;
 constexpr int I8_MAX_STAGES = 12;
 constexpr uint32_t I8_A_BYTES = 128u * 128u;
-constexpr uint32_t I8_EPI_STAGE = 2048;  // per epilogue warp: 16 tokens x 32 channels (two bf16 halves or one fp32)
+constexpr uint32_t I8_EPI_STAGE = 4096 + 1024;  // per epilogue warp: 32 tokens x 32 channels (two bf16 halves or one fp32), a tile's xs
 
 __host__ __device__ constexpr size_t i8_smem_bytes(int stages, uint32_t stage_bytes) {
     return 1024 + static_cast<size_t>(stages) * stage_bytes + 512 + 4 * I8_EPI_STAGE;
@@ -259,19 +259,30 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
             }
             const float wsc = n < a.N ? __ldg(a.ws + n) : 0.0f;
             const float bv = (a.bias && n < a.N) ? bf16_bits_to_f32(a.bias[n]) : 0.0f;
-            for (int c0 = 0; c0 < m_end; c0 += 16) {
-                uint32_t v[16];
-                tmem_ld16(acc + c0, v);
-                float f[16];
+            float* xs_s = reinterpret_cast<float*>(stg + 4096);  // this tile's token scales
+            __syncwarp();
+            for (int i = lane; i < a.bn; i += 32) xs_s[i] = __ldg(a.xs + min(m0 + i, a.M - 1));
+            __syncwarp();
+            for (int c0 = 0; c0 < m_end; c0 += 32) {
+                uint32_t v[2][16];
+                tmem_ld16(acc + c0, v[0]);
+                if (c0 + 16 < a.bn) tmem_ld16(acc + c0 + 16, v[1]);
+                tmem_wait_ld();
+                reg_pin(v[0]);
+                reg_pin(v[1]);
+                float f[32];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] = __ldg(a.xs + min(m0 + c0 + i, a.M - 1));
-                tmem_wait_ld_pin(v);
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 x4 = *reinterpret_cast<const float4*>(xs_s + c0 + i);
+                    const float xs4[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] = fmaf(static_cast<float>(static_cast<int>(v[i])) * f[i], wsc, bv);
+                    for (int k = 0; k < 4; ++k)
+                        f[i + k] = fmaf(static_cast<float>(static_cast<int>(v[(i + k) / 16][(i + k) & 15])) * xs4[k], wsc, bv);
+                }
                 if (a.tma_store) {
                     if (n0 < a.N) {  // the same for the whole warp
-                        const bool half = !a.y_f32;  // bf16: two alternating 1 KB halves
-                        uint8_t* dst = stg + ((half && (chunk & 1)) ? 1024 : 0);
+                        const bool half = !a.y_f32;  // bf16: two alternating 2 KB halves
+                        uint8_t* dst = stg + ((half && (chunk & 1)) ? 2048 : 0);
                         if (lane == 0) {
                             if (half) bulk_wait_read<1>();
                             else bulk_wait_read<0>();
@@ -280,21 +291,21 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
                         if (half) {
                             uint16_t* d = reinterpret_cast<uint16_t*>(dst);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) d[i * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
+                            for (int i = 0; i < 32; ++i) d[i * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
                         } else {
                             float* d = reinterpret_cast<float*>(dst);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) d[i * 32 + lane] = f[i];
+                            for (int i = 0; i < 32; ++i) d[i * 32 + lane] = f[i];
                         }
                         fence_proxy_async();
                         __syncwarp();
-                        // tokens past M are clipped by the store (bn is a multiple of 16)
+                        // tokens past M are clipped by the store (bn is a multiple of 32 here)
                         if (lane == 0) tma_store_2d(&tm_y, dst, n0, m0 + c0);
                         ++chunk;
                     }
                 } else if (n < a.N) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < 32; ++i) {
                         const int m = m0 + c0 + i;
                         if (c0 + i < m_end) {
                             if (a.y_f32) static_cast<float*>(a.y)[static_cast<int64_t>(m) * a.N + n] = f[i];
