@@ -192,22 +192,21 @@ __device__ __forceinline__ uint4 norm_rope_row(uint4 raw, const float2 (&w)[4], 
     float2 p[4], y[4], d[4];
     float e[4];
     const float k = r * 5.364418029785156e-7f;  // 9 * 2^-24 r
-    const float2 r2 = make_float2(r, r);
     bool near = false;  // a bf16 midpoint lies within E
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = mul_f32x2(x[i], w[i]);  // exact: 8 x 8 bits
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if constexpr (INTER) p[i] = make_float2(-x[i].y, x[i].x);
+        if constexpr (INTER) p[i] = make_float2(-x[i].y, x[i].x);  // signs fold into the products
         else p[i] = make_float2(__shfl_sync(0xffffffffu, x[i].x, R.src), __shfl_sync(0xffffffffu, x[i].y, R.src));
     }
     uint4 out;
     uint32_t* o = reinterpret_cast<uint32_t*>(&out);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 c = INTER ? make_float2(R.c[i], R.c[i]) : make_float2(R.c[(2 * i) & RM], R.c[(2 * i + 1) & RM]);
-        const float2 s = INTER ? make_float2(R.s[i], R.s[i]) : make_float2(R.s[(2 * i) & RM], R.s[(2 * i + 1) & RM]);
-        y[i] = mul_f32x2(fma_f32x2(x[i], c, mul_f32x2(p[i], s)), r2);
+        const float c0 = R.c[INTER ? i : (2 * i) & RM], c1 = INTER ? c0 : R.c[(2 * i + 1) & RM];
+        const float s0 = R.s[INTER ? i : (2 * i) & RM], s1 = INTER ? s0 : R.s[(2 * i + 1) & RM];
+        y[i] = make_float2(fmaf(x[i].x, c0, p[i].x * s0) * r, fmaf(x[i].y, c1, p[i].y * s1) * r);
         // minus the midpoint above: the upper half's bits, 0x8000 below, the sign turned
         const float2 mid = make_float2(__uint_as_float((__float_as_uint(y[i].x) & 0xFFFF0000u) ^ 0x80008000u),
                                        __uint_as_float((__float_as_uint(y[i].y) & 0xFFFF0000u) ^ 0x80008000u));
@@ -271,47 +270,52 @@ __device__ __forceinline__ void load_weight8(const uint16_t* w, int l, float2 (&
                  : make_float2(1.0f, 1.0f);
 }
 
-// grid (tokens, splits of the token's rows); a CTA takes rows y, y + splits, ...
-// in warp-sized bites of 32 / LPR rows.
+// The rows of one side that this warp takes: bites of RPW heads, every `step`-th
+// from `b`; two bites are in flight.
+template <int D, bool INTER>
+__device__ __forceinline__ void norm_rope_side(const HeadRows& S, int64_t token, int b, int step, bool rope, const RopeArgs& a,
+                                               const RopeLane<D, INTER>& R, const TokenTurns& T, int lane) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    const int l = lane & (LPR - 1);
+    int h = b * RPW + lane / LPR;
+    if (b * RPW >= S.heads) return;
+    float2 w[4];
+    load_weight8(S.w, l, w);
+    const uint16_t* x = S.x + token * S.stride + static_cast<int64_t>(h) * D + 8 * l;
+    uint16_t* o = S.out + token * S.out_stride + static_cast<int64_t>(h) * D + 8 * l;
+    const int hs = step * RPW, left = (S.heads - b * RPW + hs - 1) / hs;  // bites of this warp
+    uint4 r0 = h < S.heads ? *reinterpret_cast<const uint4*>(x) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < left; ++i) {
+        x += hs * D;
+        uint4 r1 = make_uint4(0u, 0u, 0u, 0u);
+        if (h + hs < S.heads) r1 = *reinterpret_cast<const uint4*>(x);
+        const uint4 y = norm_rope_row<D, INTER>(r0, w, S.w != nullptr, rope, a, R, T);
+        if (h < S.heads) *reinterpret_cast<uint4*>(o) = y;
+        o += hs * D;
+        h += hs;
+        r0 = r1;
+    }
+}
+
+// grid (tokens, splits of the token's rows).
 template <int D, bool INTER>
 __global__ void __launch_bounds__(KV_THREADS) qk_norm_rope_kernel(const HeadRows q, const HeadRows k, const RopeArgs a,
                                                                   int64_t tokens) {
-    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    constexpr int RPW = 32 / (D / 8);
     __shared__ TokenTurns turns;
     grid_dependency_sync();
     const int64_t token = blockIdx.x;
     const bool rope = a.pos != nullptr;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (LPR - 1), sub = lane / LPR;
-    const int step = gridDim.y * (KV_THREADS / 32);
-    const int bites_q = (q.heads + RPW - 1) / RPW, bites = bites_q + (k.heads + RPW - 1) / RPW;
-    auto fetch = [&](int b) {
-        const bool isq = b < bites_q;
-        const HeadRows& S = isq ? q : k;
-        const int h = (isq ? b : b - bites_q) * RPW + sub;
-        return b < bites && h < S.heads ? *reinterpret_cast<const uint4*>(S.x + token * S.stride + static_cast<int64_t>(h) * D + 8 * l)
-                                        : make_uint4(0u, 0u, 0u, 0u);
-    };
-    int b = blockIdx.y * (KV_THREADS / 32) + warp;
-    uint4 raw = fetch(b);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (rope) token_turns(a, token, turns);
     __syncthreads();
     RopeLane<D, INTER> R;
     R.load(a, turns, rope, lane);
-    float2 w[4];
-    int held = -1;  // whose weight w holds
-    for (; b < bites; b += step) {
-        const uint4 next = fetch(b + step);
-        const bool isq = b < bites_q;
-        const HeadRows& S = isq ? q : k;
-        if (held != static_cast<int>(isq)) {
-            load_weight8(S.w, l, w);
-            held = static_cast<int>(isq);
-        }
-        const int h = (isq ? b : b - bites_q) * RPW + sub;
-        const uint4 o = norm_rope_row<D, INTER>(raw, w, S.w != nullptr, rope, a, R, turns);
-        if (h < S.heads) *reinterpret_cast<uint4*>(S.out + token * S.out_stride + static_cast<int64_t>(h) * D + 8 * l) = o;
-        raw = next;
-    }
+    const int step = gridDim.y * (KV_THREADS / 32), first = blockIdx.y * (KV_THREADS / 32) + warp;
+    norm_rope_side<D, INTER>(q, token, first, step, rope, a, R, turns, lane);
+    // the keys' bites go on where the queries' ended
+    const int bites_q = (q.heads + RPW - 1) / RPW, skip = bites_q % step;
+    norm_rope_side<D, INTER>(k, token, first >= skip ? first - skip : first + step - skip, step, rope, a, R, turns, lane);
 }
 
 // The cached position of token i of sequence b: its page and place, or -1
