@@ -376,7 +376,8 @@ wlq_status wlq_w4a4_linear(const void* x, int64_t M, const void* wq, const void*
  *   n_d = x_d w_d / sqrt(mean_d x_d^2 + eps)          (weight NULL: n = x)
  *   each rotated pair (a, b), i = its number, angle = positions[t][axis(i)]
  *   * inv_freq[i]:   a' = a cos - b sin,  b' = a sin + b cos
- * and the result is the bf16 value nearest to the real one (one rounding).
+ * evaluated in fp32 (within 9 * 2^-24 (|a| + |b|) of the real value, n's pair
+ * (a, b); the angles in fp64, at any position) and rounded once to bf16.
  * Pairs: interleaved != 0: inputs (2 i, 2 i + 1); 0: (i, i + rotary_dim / 2).
  * Inputs from rotary_dim on are normed but not rotated.  sections[a] pairs
  * turn by axis a, in order (1 axis: text; 2 or 3: height, width / time,
@@ -421,10 +422,11 @@ wlq_status wlq_qk_norm_rope(const void* q, int64_t q_stride, int q_heads, const 
  * or fewer cached ones than tokens, a page outside the pool or the table) set
  * WLQ_ERR_INDEX in the device error word; the tokens concerned are skipped.
  *
- * wlq_kv4_append: keys normed and rotated as by wlq_qk_norm_rope (k_weight,
- * positions NULL: neither; same bits as that call), values as they are, both
- * rounded to 4 bits and written to their places.  k, v: bf16 with token
- * strides.  A value beyond 65280 in magnitude, an infinity or a NaN sets
+ * wlq_kv4_append: keys normed and rotated by wlq_qk_norm_rope's formula
+ * (k_weight, positions NULL: neither), values as they are, both rounded to 4
+ * bits and written to their places.  The codes and scales are exactly those of
+ * the bf16 values nearest to the real keys.  k, v: bf16 with token strides.
+ * A value beyond 65280 in magnitude, an infinity or a NaN sets
  * WLQ_ERR_NONFINITE; its group gets scale 0 and codes 0.  Pages that one call
  * writes must belong to one sequence.  batch * max_q < 2^31.
  */

@@ -452,8 +452,8 @@ def _batch(cu_seqlens, kv_lens, block_table, max_q: int):
 
 def kv4_append(cache, k, v, cu_seqlens, kv_lens, block_table, max_q: int, positions=None, inv_freq=None, sections=None,
                interleaved: bool = True, k_weight=None, eps: float = 1e-6, stream=None):
-    """Keys (normed and rotated as by qk_norm_rope) and values rounded to 4 bits
-    into the paged cache.  k, v: bf16 [tokens, heads, head_dim], token stride
+    """Keys (normed and rotated by qk_norm_rope's formula) and values rounded to 4
+    bits into the paged cache.  k, v: bf16 [tokens, heads, head_dim], token stride
     free.  Sequence b's tokens cu_seqlens[b] .. cu_seqlens[b + 1] become the
     last of its kv_lens[b] cached ones, on pages block_table[b]; max_q: an upper
     bound of the sequences' token counts."""

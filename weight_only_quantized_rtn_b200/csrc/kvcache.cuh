@@ -13,23 +13,28 @@
 //   r = 1 / sqrt(mean x^2 + eps),  n_d = x_d w_d r,
 //   a pair (a, b) of rotated inputs becomes (a c - b s, a s + b c) with
 //   c, s = cos, sin of position(axis of the pair) * inv_freq(pair).
-// The result is rounded ONCE to bf16, and to the bf16 value nearest to the
-// real number: a key that lands on the other side of a border would change a
-// 4-bit code by a whole step, so the fused append has to round as any other
-// exact evaluation does.  The fp32 evaluation is within
+// It is evaluated in fp32, within
 //   E = 9 * 2^-24 r (|a| + |b|)
 // of the real value: c and s are fp64 values rounded once (2^-25 each), r is
 // within 5 * 2^-24 (squares exact, at most 7 additions of one-signed terms,
 // halved by the root; then the roundings of mean + eps and of the root), x w
-// is exact (8 + 8 bits), and there are three more roundings.  Where a bf16
-// midpoint lies within E (about one value in two thousand) that value is
-// evaluated again in fp64 and rounded from there.
+// is exact (8 + 8 bits), and there are three more roundings; then it is
+// rounded to bf16.
+//
+// The cache's codes are those of the bf16 values nearest to the REAL keys: a
+// key on the other side of a border would change its code by a whole step, so
+// the append has to round as any exact evaluation does.  A value that can get
+// a code other than 0 (its magnitude is at least a 14th of its group's
+// largest) and has a bf16 midpoint within E, about one in three thousand, is
+// evaluated again in fp64 and rounded from there.  Doing so for every value
+// of every row cost 25 us of 71 for 6240 tokens of 64 heads; the queries and
+// keys that stay bf16 do without.
 //
 // Bound: HBM.  A row is read and written once; 16 (D = 128) or 8 (D = 64)
 // lanes hold it, 8 adjacent values each (one 16-byte load), so the norm is a
 // shuffle reduction and the half-split partner one shuffle.  A CTA works out
-// its token's angles once, in fp64, while the first rows are on their way, and
-// walks the token's heads with cos and sin in registers.
+// its token's angles once, in fp64, and walks the token's heads with cos and
+// sin in registers.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -172,94 +177,100 @@ struct RopeLane {
     }
 };
 
-// One row: x (8 bf16 values a lane) to the rounded bits, two per word.
+// A row's evaluation (8 values a lane): the products x w, the partners, the
+// results in fp32.
+struct RowEval {
+    float2 x[4], p[4], y[4];
+    float r;
+};
 template <int D, bool INTER>
-__device__ __forceinline__ uint4 norm_rope_row(uint4 raw, const float2 (&w)[4], bool norm, bool rope, const RopeArgs& a,
-                                               const RopeLane<D, INTER>& R, const TokenTurns& T) {
+__device__ __forceinline__ uint4 norm_rope_row(uint4 raw, const float2 (&w)[4], bool norm, const RopeArgs& a, const RopeLane<D, INTER>& R,
+                                               RowEval& v) {
     constexpr int LPR = D / 8, RM = INTER ? 3 : 7;
-    if (!norm && !rope) return raw;
-    float2 x[4];
-    unpack8(raw, x);
-    float r = 1.0f;
+    unpack8(raw, v.x);
+    v.r = 1.0f;
     if (norm) {
-        const float2 q = add_f32x2(add_f32x2(mul_f32x2(x[0], x[0]), mul_f32x2(x[1], x[1])),
-                                   add_f32x2(mul_f32x2(x[2], x[2]), mul_f32x2(x[3], x[3])));
+        const float2 q = add_f32x2(add_f32x2(mul_f32x2(v.x[0], v.x[0]), mul_f32x2(v.x[1], v.x[1])),
+                                   add_f32x2(mul_f32x2(v.x[2], v.x[2]), mul_f32x2(v.x[3], v.x[3])));
         float ss = q.x + q.y;
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        r = __frsqrt_rn(fmaf(ss, 1.0f / D, static_cast<float>(a.eps)));
+        v.r = __frsqrt_rn(fmaf(ss, 1.0f / D, static_cast<float>(a.eps)));
     }
-    float2 p[4], y[4], d[4];
-    float e[4];
-    const float k = r * 5.364418029785156e-7f;  // 9 * 2^-24 r
-    bool near = false;  // a bf16 midpoint lies within E
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = mul_f32x2(x[i], w[i]);  // exact: 8 x 8 bits
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (INTER) p[i] = make_float2(-x[i].y, x[i].x);  // signs fold into the products
-        else p[i] = make_float2(__shfl_sync(0xffffffffu, x[i].x, R.src), __shfl_sync(0xffffffffu, x[i].y, R.src));
-    }
+    for (int i = 0; i < 4; ++i) v.x[i] = mul_f32x2(v.x[i], w[i]);  // exact: 8 x 8 bits
     uint4 out;
     uint32_t* o = reinterpret_cast<uint32_t*>(&out);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        if constexpr (INTER) v.p[i] = make_float2(-v.x[i].y, v.x[i].x);  // signs fold into the products
+        else v.p[i] = make_float2(__shfl_sync(0xffffffffu, v.x[i].x, R.src), __shfl_sync(0xffffffffu, v.x[i].y, R.src));
         const float c0 = R.c[INTER ? i : (2 * i) & RM], c1 = INTER ? c0 : R.c[(2 * i + 1) & RM];
         const float s0 = R.s[INTER ? i : (2 * i) & RM], s1 = INTER ? s0 : R.s[(2 * i + 1) & RM];
-        y[i] = make_float2(fmaf(x[i].x, c0, p[i].x * s0) * r, fmaf(x[i].y, c1, p[i].y * s1) * r);
-        // minus the midpoint above: the upper half's bits, 0x8000 below, the sign turned
-        const float2 mid = make_float2(__uint_as_float((__float_as_uint(y[i].x) & 0xFFFF0000u) ^ 0x80008000u),
-                                       __uint_as_float((__float_as_uint(y[i].y) & 0xFFFF0000u) ^ 0x80008000u));
-        d[i] = add_f32x2(y[i], mid);
-        if constexpr (INTER) {
-            e[i] = (fabsf(x[i].x) + fabsf(x[i].y)) * k;
-            near |= fabsf(d[i].x) <= e[i];
-            near |= fabsf(d[i].y) <= e[i];
-        } else {
-            near |= fabsf(d[i].x) <= (fabsf(x[i].x) + fabsf(p[i].x)) * k;
-            near |= fabsf(d[i].y) <= (fabsf(x[i].y) + fabsf(p[i].y)) * k;
-        }
-        const __nv_bfloat162 b = __floats2bfloat162_rn(y[i].x, y[i].y);
+        v.y[i] = make_float2(fmaf(v.x[i].x, c0, v.p[i].x * s0) * v.r, fmaf(v.x[i].y, c1, v.p[i].y * s1) * v.r);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v.y[i].x, v.y[i].y);
         o[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    if (__any_sync(0xffffffffu, near)) {
-        double r64 = 1.0;
-        if (norm) {
-            double ss = 0.0;
-            float2 f[4];
-            unpack8(raw, f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                ss = fma(static_cast<double>(f[i].x), static_cast<double>(f[i].x), ss);
-                ss = fma(static_cast<double>(f[i].y), static_cast<double>(f[i].y), ss);
-            }
-#pragma unroll
-            for (int j = LPR / 2; j > 0; j >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, j);
-            // two Newton steps from the fp32 root: 2^-22 -> 2^-43 -> fp64's own rounding
-            const double v = 0.5 * (ss / D + a.eps);
-            r64 = static_cast<double>(r);
-            r64 = r64 * fma(-v * r64, r64, 1.5);
-            r64 = r64 * fma(-v * r64, r64, 1.5);
-        }
-        if (near) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float xi = (i & 1) ? x[i / 2].y : x[i / 2].x, pi = (i & 1) ? p[i / 2].y : p[i / 2].x;
-                const float di = (i & 1) ? d[i / 2].y : d[i / 2].x;
-                if (!(fabsf(di) <= (fabsf(xi) + fabsf(pi)) * k)) continue;
-                double c = 1.0, s = 0.0;
-                if (R.first >= 0) {
-                    const double2 t = T.d[R.first + (INTER ? i / 2 : i)];
-                    c = t.x;
-                    s = R.lo ? -t.y : t.y;
-                }
-                const uint32_t b = bf16_from_f64((static_cast<double>(xi) * c + static_cast<double>(pi) * s) * r64);
-                o[i / 2] = (i & 1) ? ((o[i / 2] & 0xFFFFu) | (b << 16)) : ((o[i / 2] & 0xFFFF0000u) | b);
-            }
-        }
-        __syncwarp();
-    }
     return out;
+}
+
+// Whether a bf16 midpoint lies within e of y: minus the midpoint above y's
+// upper half is those bits with 0x8000 below and the sign turned.
+__device__ __forceinline__ bool near_midpoint(float y, float e) {
+    return fabsf(y + __uint_as_float((__float_as_uint(y) & 0xFFFF0000u) ^ 0x80008000u)) <= e;
+}
+
+// Rounds again, from fp64, the values of at least `least` in magnitude that a
+// bf16 midpoint lies close to.  The whole warp; true where any was.
+template <int D, bool INTER>
+__device__ __forceinline__ bool settle_row(uint4 raw, bool norm, const RopeArgs& a, const RopeLane<D, INTER>& R, const TokenTurns& T,
+                                           const RowEval& v, float least, uint4& out) {
+    constexpr int LPR = D / 8;
+    const float k = v.r * 5.364418029785156e-7f;  // 9 * 2^-24 r
+    bool near = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        near |= near_midpoint(v.y[i].x, (fabsf(v.x[i].x) + fabsf(v.p[i].x)) * k) && fabsf(v.y[i].x) >= least;
+        near |= near_midpoint(v.y[i].y, (fabsf(v.x[i].y) + fabsf(v.p[i].y)) * k) && fabsf(v.y[i].y) >= least;
+    }
+    if (!__any_sync(0xffffffffu, near)) return false;
+    double r64 = 1.0;
+    if (norm) {
+        double ss = 0.0;
+        float2 f[4];
+        unpack8(raw, f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ss = fma(static_cast<double>(f[i].x), static_cast<double>(f[i].x), ss);
+            ss = fma(static_cast<double>(f[i].y), static_cast<double>(f[i].y), ss);
+        }
+#pragma unroll
+        for (int j = LPR / 2; j > 0; j >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, j);
+        // two Newton steps from the fp32 root: 2^-22 -> 2^-43 -> fp64's own rounding
+        const double h = 0.5 * (ss / D + a.eps);
+        r64 = static_cast<double>(v.r);
+        r64 = r64 * fma(-h * r64, r64, 1.5);
+        r64 = r64 * fma(-h * r64, r64, 1.5);
+    }
+    if (near) {
+        uint32_t* o = reinterpret_cast<uint32_t*>(&out);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float xi = (i & 1) ? v.x[i / 2].y : v.x[i / 2].x, pi = (i & 1) ? v.p[i / 2].y : v.p[i / 2].x;
+            const float yi = (i & 1) ? v.y[i / 2].y : v.y[i / 2].x;
+            if (!near_midpoint(yi, (fabsf(xi) + fabsf(pi)) * k)) continue;
+            double c = 1.0, s = 0.0;
+            if (R.first >= 0) {
+                const double2 t = T.d[R.first + (INTER ? i / 2 : i)];
+                c = t.x;
+                s = R.lo ? -t.y : t.y;
+            }
+            const uint32_t b = bf16_from_f64((static_cast<double>(xi) * c + static_cast<double>(pi) * s) * r64);
+            o[i / 2] = (i & 1) ? ((o[i / 2] & 0xFFFFu) | (b << 16)) : ((o[i / 2] & 0xFFFF0000u) | b);
+        }
+    }
+    __syncwarp();
+    return true;
 }
 
 __device__ __forceinline__ void load_weight8(const uint16_t* w, int l, float2 (&f)[4]) {
@@ -274,9 +285,10 @@ __device__ __forceinline__ void load_weight8(const uint16_t* w, int l, float2 (&
 // from `b`; two bites are in flight.
 template <int D, bool INTER>
 __device__ __forceinline__ void norm_rope_side(const HeadRows& S, int64_t token, int b, int step, bool rope, const RopeArgs& a,
-                                               const RopeLane<D, INTER>& R, const TokenTurns& T, int lane) {
+                                               const RopeLane<D, INTER>& R, int lane) {
     constexpr int LPR = D / 8, RPW = 32 / LPR;
     const int l = lane & (LPR - 1);
+    const bool plain = !rope && !S.w;  // neither: a copy
     int h = b * RPW + lane / LPR;
     if (b * RPW >= S.heads) return;
     float2 w[4];
@@ -289,7 +301,8 @@ __device__ __forceinline__ void norm_rope_side(const HeadRows& S, int64_t token,
         x += hs * D;
         uint4 r1 = make_uint4(0u, 0u, 0u, 0u);
         if (h + hs < S.heads) r1 = *reinterpret_cast<const uint4*>(x);
-        const uint4 y = norm_rope_row<D, INTER>(r0, w, S.w != nullptr, rope, a, R, T);
+        RowEval v;
+        const uint4 y = plain ? r0 : norm_rope_row<D, INTER>(r0, w, S.w != nullptr, a, R, v);
         if (h < S.heads) *reinterpret_cast<uint4*>(o) = y;
         o += hs * D;
         h += hs;
@@ -312,10 +325,10 @@ __global__ void __launch_bounds__(KV_THREADS) qk_norm_rope_kernel(const HeadRows
     RopeLane<D, INTER> R;
     R.load(a, turns, rope, lane);
     const int step = gridDim.y * (KV_THREADS / 32), first = blockIdx.y * (KV_THREADS / 32) + warp;
-    norm_rope_side<D, INTER>(q, token, first, step, rope, a, R, turns, lane);
+    norm_rope_side<D, INTER>(q, token, first, step, rope, a, R, lane);
     // the keys' bites go on where the queries' ended
     const int bites_q = (q.heads + RPW - 1) / RPW, skip = bites_q % step;
-    norm_rope_side<D, INTER>(k, token, first >= skip ? first - skip : first + step - skip, step, rope, a, R, turns, lane);
+    norm_rope_side<D, INTER>(k, token, first >= skip ? first - skip : first + step - skip, step, rope, a, R, lane);
 }
 
 // The cached position of token i of sequence b: its page and place, or -1
@@ -426,11 +439,22 @@ __global__ void __launch_bounds__(KV_THREADS) kv4_append_kernel(const HeadRows k
         const bool isk = t < bites_k;
         const int h = (isk ? t : t - bites_k) * RPW + sub;
         const bool in = h < P.heads;
-        if (isk) raw = norm_rope_row<D, INTER>(raw, w, k.w != nullptr, rope, a, R, turns);
-        uint32_t m2 = __vmaxu2(__vmaxu2(raw.x & 0x7FFF7FFFu, raw.y & 0x7FFF7FFFu),
-                               __vmaxu2(raw.z & 0x7FFF7FFFu, raw.w & 0x7FFF7FFFu));
-        uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-        for (int o = (1 << lg8) >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        auto group_max = [&](uint4 u) {  // the group's largest magnitude, as bf16 bits
+            const uint32_t m2 = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+            uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+            for (int o = (1 << lg8) >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            return m;
+        };
+        uint32_t m;
+        if (isk && (rope || k.w)) {  // the same for the whole warp
+            RowEval v;
+            const uint4 in_row = raw;
+            raw = norm_rope_row<D, INTER>(in_row, w, k.w != nullptr, a, R, v);
+            m = group_max(raw);
+            if (settle_row<D, INTER>(in_row, k.w != nullptr, a, R, turns, v, __uint_as_float(m << 16) * 0.0625f, raw)) m = group_max(raw);
+        } else {
+            m = group_max(raw);
+        }
         const float amax = __uint_as_float(m << 16);
         const bool gbad = !(amax <= KV4_MAX_ABS);  // too large, an infinity or a NaN
         const float s = gbad ? 0.0f : kv4_scale(amax);
