@@ -56,6 +56,22 @@ unsigned head_splits(int64_t tokens, int bites, int sms) {
     return static_cast<unsigned>(std::max<int64_t>(1, std::min(most, want)));
 }
 
+// The cache kernels' grid: a CTA takes a piece of `tpc` tokens of a sequence --
+// several where there are enough of them, so that looking up their places (three
+// loads that depend on each other) is paid once.
+struct KvGrid {
+    dim3 grid;
+    int tpc, pieces;
+};
+KvGrid kv_grid(int batch, int max_q, int64_t tokens, int bites, int tpc, int sms) {
+    KvGrid g;
+    g.tpc = std::min<int64_t>(tokens, static_cast<int64_t>(batch) * max_q) >= 16ll * sms && max_q >= tpc ? tpc : 1;
+    g.pieces = static_cast<int>(cdiv(max_q, g.tpc));
+    const int64_t units = static_cast<int64_t>(batch) * g.pieces;
+    g.grid = dim3(static_cast<unsigned>(units), head_splits(std::min(units, tokens), bites, sms));
+    return g;
+}
+
 wlq_status check_batch(const int32_t* cu, const int32_t* kv_lens, int batch, int max_q, const int32_t* table,
                        int64_t table_width, int64_t tokens, wlq::KvBatch* out) {
     if (batch < 0 || max_q < 0 || tokens < 0 || table_width < 0)
@@ -137,7 +153,7 @@ DecPlan dec_plan(int64_t tokens, int batch, int max_q, int64_t max_kv, int q_hea
 template <int D, int NT, int G>
 cudaError_t launch_dec(unsigned grid, cudaStream_t s, const wlq::AttnArgs& a, DeviceInfo* d) {
     constexpr size_t smem = wlq::dec_smem_bytes<D, NT, G>();
-    constexpr int kid = 28 + (D == 128 ? 8 : 0) + (NT == 2 ? 4 : 0) + (G == 4 ? 2 : G == 2 ? 1 : 0);  // 28..39
+    constexpr int kid = 64 + (D == 128 ? 6 : 0) + (NT == 2 ? 3 : 0) + (G == 4 ? 2 : G == 2 ? 1 : 0);  // 64..75
     if (!d->smem_set[kid]) {
         const cudaError_t e = cudaFuncSetAttribute(wlq::kv4_decode_kernel<D, NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
@@ -248,17 +264,16 @@ wlq_status wlq_kv4_append(const void* k, int64_t k_stride, const void* v, int64_
     if ((st = current_device(&dev, &d)) != WLQ_OK) return st;
     const wlq::HeadRows K{static_cast<const uint16_t*>(k), k_stride, heads, static_cast<const uint16_t*>(k_weight), nullptr, 0};
     const wlq::HeadRows V{static_cast<const uint16_t*>(v), v_stride, heads, nullptr, nullptr, 0};
-    const int bites = static_cast<int>(2 * cdiv(heads, 32 / (head_dim / 8)));
-    const int64_t units = static_cast<int64_t>(batch) * max_q;
-    const dim3 grid(static_cast<unsigned>(units), head_splits(std::min(units, tokens), bites, d->sms));
+    const KvGrid g = kv_grid(batch, max_q, tokens, static_cast<int>(2 * cdiv(heads, 32 / (head_dim / 8))), 2, d->sms);
+    const dim3 grid = g.grid;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (head_dim == 128)
-        e = interleaved ? launch_k(wlq::kv4_append_kernel<128, true>, grid, wlq::KV_THREADS, 0, s, K, V, a, B, P)
-                        : launch_k(wlq::kv4_append_kernel<128, false>, grid, wlq::KV_THREADS, 0, s, K, V, a, B, P);
+        e = interleaved ? launch_k(wlq::kv4_append_kernel<128, true>, grid, wlq::KV_THREADS, 0, s, K, V, a, B, P, g.tpc, g.pieces)
+                        : launch_k(wlq::kv4_append_kernel<128, false>, grid, wlq::KV_THREADS, 0, s, K, V, a, B, P, g.tpc, g.pieces);
     else
-        e = interleaved ? launch_k(wlq::kv4_append_kernel<64, true>, grid, wlq::KV_THREADS, 0, s, K, V, a, B, P)
-                        : launch_k(wlq::kv4_append_kernel<64, false>, grid, wlq::KV_THREADS, 0, s, K, V, a, B, P);
+        e = interleaved ? launch_k(wlq::kv4_append_kernel<64, true>, grid, wlq::KV_THREADS, 0, s, K, V, a, B, P, g.tpc, g.pieces)
+                        : launch_k(wlq::kv4_append_kernel<64, false>, grid, wlq::KV_THREADS, 0, s, K, V, a, B, P, g.tpc, g.pieces);
     return e == cudaSuccess ? WLQ_OK : cuda_fail(e, "kv4_append launch");
 }
 
@@ -279,13 +294,12 @@ wlq_status wlq_kv4_read(const int32_t* cu_seqlens, const int32_t* kv_lens, int b
     int dev;
     DeviceInfo* d;
     if ((st = current_device(&dev, &d)) != WLQ_OK) return st;
-    const int bites = static_cast<int>(2 * cdiv(heads, 32 / (head_dim / 8)));
-    const int64_t units = static_cast<int64_t>(batch) * max_q;
-    const dim3 grid(static_cast<unsigned>(units), head_splits(std::min(units, tokens), bites, d->sms));
+    const KvGrid g = kv_grid(batch, max_q, tokens, static_cast<int>(cdiv(heads, 32 / (head_dim / 8))), wlq::KV_TPC, d->sms);
+    const dim3 grid = g.grid;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint16_t *ko = static_cast<uint16_t*>(k_out), *vo = static_cast<uint16_t*>(v_out);
-    const cudaError_t e = head_dim == 128 ? launch_k(wlq::kv4_read_kernel<128>, grid, wlq::KV_THREADS, 0, s, ko, vo, B, P)
-                                          : launch_k(wlq::kv4_read_kernel<64>, grid, wlq::KV_THREADS, 0, s, ko, vo, B, P);
+    const cudaError_t e = head_dim == 128 ? launch_k(wlq::kv4_read_kernel<128>, grid, wlq::KV_THREADS, 0, s, ko, vo, B, P, g.tpc, g.pieces)
+                                          : launch_k(wlq::kv4_read_kernel<64>, grid, wlq::KV_THREADS, 0, s, ko, vo, B, P, g.tpc, g.pieces);
     return e == cudaSuccess ? WLQ_OK : cuda_fail(e, "kv4_read launch");
 }
 

@@ -126,8 +126,8 @@ struct TokenTurns {
     float2 f[ROPE_MAX_PAIRS];
     double2 d[ROPE_MAX_PAIRS];
 };
-__device__ __forceinline__ void token_turns(const RopeArgs& a, int64_t token, TokenTurns& T) {
-    for (int i = threadIdx.x; i < a.pairs; i += blockDim.x) {
+__device__ __forceinline__ void token_turns(const RopeArgs& a, int64_t token, TokenTurns& T, int first = threadIdx.x, int step = KV_THREADS) {
+    for (int i = first; i < a.pairs; i += step) {
         int ax = 0;
 #pragma unroll
         for (int k = 0; k < ROPE_MAX_AXES - 1; ++k)
@@ -401,75 +401,86 @@ __device__ __forceinline__ uint32_t kv4_quantize(const float2 (&x)[4], float s) 
     return lo | (hi << 4);
 }
 
-// grid (max_q * batch, splits of the token's 2 H rows): key rows, then value
-// rows, a warp-sized bite at a time.
+// grid (batch * the sequences' pieces of `tpc` tokens, splits of a token's 2 H
+// rows): the places of a piece's tokens are looked up side by side, then each
+// token's key rows and value rows are taken a warp-sized bite at a time.
+constexpr int KV_TPC = 4;  // tokens of a CTA at most
+
 template <int D, bool INTER>
 __global__ void __launch_bounds__(KV_THREADS) kv4_append_kernel(const HeadRows k, const HeadRows v, const RopeArgs a,
-                                                                const KvBatch B, const Kv4Pool P) {
+                                                                const KvBatch B, const Kv4Pool P, int tpc, int pieces) {
     constexpr int LPR = D / 8, RPW = 32 / LPR;
-    __shared__ TokenTurns turns;
+    __shared__ TokenTurns turns[KV_TPC];
+    __shared__ KvSlot slots[KV_TPC];
     grid_dependency_sync();
-    const int b = blockIdx.x / B.max_q, i = blockIdx.x - b * B.max_q;
-    KvSlot slot;
-    if (!kv_slot(B, P, b, i, slot)) return;  // the same for the whole CTA
-    const bool rope = a.pos != nullptr;
+    const int b = blockIdx.x / pieces, i0 = (blockIdx.x - b * pieces) * tpc;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (LPR - 1), sub = lane / LPR;
-    const int step = gridDim.y * (KV_THREADS / 32);
-    const int bites_k = (P.heads + RPW - 1) / RPW;
-    auto fetch = [&](int t) {
-        const bool isk = t < bites_k;
-        const HeadRows& S = isk ? k : v;
-        const int h = (isk ? t : t - bites_k) * RPW + sub;
-        return t < 2 * bites_k && h < P.heads ? *reinterpret_cast<const uint4*>(S.x + slot.row * S.stride + static_cast<int64_t>(h) * D + 8 * l)
-                                              : make_uint4(0u, 0u, 0u, 0u);
-    };
-    int t = blockIdx.y * (KV_THREADS / 32) + warp;
-    uint4 next = fetch(t);
-    if (rope) token_turns(a, slot.row, turns);
+    const bool rope = a.pos != nullptr;
+    if (threadIdx.x < tpc && !(i0 + static_cast<int>(threadIdx.x) < B.max_q && kv_slot(B, P, b, i0 + threadIdx.x, slots[threadIdx.x])))
+        slots[threadIdx.x].page = -1;
     float2 w[4];
     load_weight8(k.w, l, w);
     __syncthreads();
-    RopeLane<D, INTER> R;
-    R.load(a, turns, rope, lane);
+    if (rope) {
+        for (int t = 0; t < tpc; ++t)  // the threads go on where the token before ended
+            if (slots[t].page >= 0) token_turns(a, slots[t].row, turns[t], (threadIdx.x + KV_THREADS - t * a.pairs % KV_THREADS) % KV_THREADS);
+        __syncthreads();
+    }
+    const int bites_k = (P.heads + RPW - 1) / RPW;
     const int lg8 = P.lg_group - 3;  // log2 of the lanes of a group
+    const int step = gridDim.y * (KV_THREADS / 32), first = blockIdx.y * (KV_THREADS / 32) + warp;
     bool bad = false;
-    for (; t < 2 * bites_k; t += step) {
-        uint4 raw = next;
-        next = fetch(t + step);
-        const bool isk = t < bites_k;
-        const int h = (isk ? t : t - bites_k) * RPW + sub;
-        const bool in = h < P.heads;
-        auto group_max = [&](uint4 u) {  // the group's largest magnitude, as bf16 bits
-            const uint32_t m2 = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
-            uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-            for (int o = (1 << lg8) >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            return m;
+    for (int tok = 0; tok < tpc; ++tok) {
+        const KvSlot slot = slots[tok];
+        if (slot.page < 0) continue;
+        auto fetch = [&](int t) {
+            const bool isk = t < bites_k;
+            const HeadRows& S = isk ? k : v;
+            const int h = (isk ? t : t - bites_k) * RPW + sub;
+            return t < 2 * bites_k && h < P.heads ? *reinterpret_cast<const uint4*>(S.x + slot.row * S.stride + static_cast<int64_t>(h) * D + 8 * l)
+                                                  : make_uint4(0u, 0u, 0u, 0u);
         };
-        uint32_t m;
-        if (isk && (rope || k.w)) {  // the same for the whole warp
-            RowEval v;
-            const uint4 in_row = raw;
-            raw = norm_rope_row<D, INTER>(in_row, w, k.w != nullptr, a, R, v);
-            m = group_max(raw);
-            if (settle_row<D, INTER>(in_row, k.w != nullptr, a, R, turns, v, __uint_as_float(m << 16) * 0.0625f, raw)) m = group_max(raw);
-        } else {
-            m = group_max(raw);
-        }
-        const float amax = __uint_as_float(m << 16);
-        const bool gbad = !(amax <= KV4_MAX_ABS);  // too large, an infinity or a NaN
-        const float s = gbad ? 0.0f : kv4_scale(amax);
-        bad |= gbad && in;
-        uint32_t word = 0x88888888u;
-        if (s > 0.0f) {
-            float2 f[4];
-            unpack8(raw, f);
-            word = kv4_quantize(f, s);
-        }
-        if (in) {
-            const int64_t row = kv_row(P, slot, h);
-            reinterpret_cast<uint32_t*>(isk ? P.k : P.v)[row * LPR + l] = word;
-            if ((l & ((1 << lg8) - 1)) == 0)
-                (isk ? P.ks : P.vs)[row * (LPR >> lg8) + (l >> lg8)] = __float2half_rn(s);
+        uint4 next = fetch(first);
+        RopeLane<D, INTER> R;
+        R.load(a, turns[tok], rope, lane);
+        for (int t = first; t < 2 * bites_k; t += step) {
+            uint4 raw = next;
+            next = fetch(t + step);
+            const bool isk = t < bites_k;
+            const int h = (isk ? t : t - bites_k) * RPW + sub;
+            const bool in = h < P.heads;
+            auto group_max = [&](uint4 u) {  // the group's largest magnitude, as bf16 bits
+                const uint32_t m2 = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+                uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+                for (int o = (1 << lg8) >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                return m;
+            };
+            uint32_t m;
+            if (isk && (rope || k.w)) {  // the same for the whole warp
+                RowEval e;
+                const uint4 in_row = raw;
+                raw = norm_rope_row<D, INTER>(in_row, w, k.w != nullptr, a, R, e);
+                m = group_max(raw);
+                if (settle_row<D, INTER>(in_row, k.w != nullptr, a, R, turns[tok], e, __uint_as_float(m << 16) * 0.0625f, raw)) m = group_max(raw);
+            } else {
+                m = group_max(raw);
+            }
+            const float amax = __uint_as_float(m << 16);
+            const bool gbad = !(amax <= KV4_MAX_ABS);  // too large, an infinity or a NaN
+            const float s = gbad ? 0.0f : kv4_scale(amax);
+            bad |= gbad && in;
+            uint32_t word = 0x88888888u;
+            if (s > 0.0f) {
+                float2 f[4];
+                unpack8(raw, f);
+                word = kv4_quantize(f, s);
+            }
+            if (in) {
+                const int64_t row = kv_row(P, slot, h);
+                reinterpret_cast<uint32_t*>(isk ? P.k : P.v)[row * LPR + l] = word;
+                if ((l & ((1 << lg8) - 1)) == 0)
+                    (isk ? P.ks : P.vs)[row * (LPR >> lg8) + (l >> lg8)] = __float2half_rn(s);
+            }
         }
     }
     if (bad) raise_error(ERRBIT_NONFINITE);
@@ -494,25 +505,31 @@ __device__ __forceinline__ uint4 kv4_values(uint32_t word, float s) {
 
 template <int D>
 __global__ void __launch_bounds__(KV_THREADS) kv4_read_kernel(uint16_t* __restrict__ k_out, uint16_t* __restrict__ v_out,
-                                                              const KvBatch B, const Kv4Pool P) {
+                                                              const KvBatch B, const Kv4Pool P, int tpc, int pieces) {
     constexpr int LPR = D / 8, RPW = 32 / LPR;
+    __shared__ KvSlot slots[KV_TPC];
     grid_dependency_sync();
-    const int b = blockIdx.x / B.max_q, i = blockIdx.x - b * B.max_q;
-    KvSlot slot;
-    if (!kv_slot(B, P, b, i, slot)) return;
+    const int b = blockIdx.x / pieces, i0 = (blockIdx.x - b * pieces) * tpc;
+    if (threadIdx.x < tpc && !(i0 + static_cast<int>(threadIdx.x) < B.max_q && kv_slot(B, P, b, i0 + threadIdx.x, slots[threadIdx.x])))
+        slots[threadIdx.x].page = -1;
+    __syncthreads();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (LPR - 1), sub = lane / LPR;
-    const int step = gridDim.y * (KV_THREADS / 32);
-    const int bites_k = (P.heads + RPW - 1) / RPW;
+    const int step = gridDim.y * (KV_THREADS / 32), bites = (P.heads + RPW - 1) / RPW;
     const int lg8 = P.lg_group - 3;
-    for (int t = blockIdx.y * (KV_THREADS / 32) + warp; t < 2 * bites_k; t += step) {
-        const bool isk = t < bites_k;
-        const int h = (isk ? t : t - bites_k) * RPW + sub;
-        if (h >= P.heads) continue;
-        const int64_t row = kv_row(P, slot, h);
-        const uint32_t word = reinterpret_cast<const uint32_t*>(isk ? P.k : P.v)[row * LPR + l];
-        const float s = __half2float((isk ? P.ks : P.vs)[row * (LPR >> lg8) + (l >> lg8)]);
-        uint16_t* out = (isk ? k_out : v_out) + (slot.row * P.heads + h) * D + 8 * l;
-        *reinterpret_cast<uint4*>(out) = kv4_values(word, s);
+    for (int tok = 0; tok < tpc; ++tok) {
+        const KvSlot slot = slots[tok];
+        if (slot.page < 0) continue;
+#pragma unroll 2
+        for (int t = blockIdx.y * (KV_THREADS / 32) + warp; t < bites; t += step) {  // a bite of key rows and of value rows
+            const int h = t * RPW + sub;
+            if (h >= P.heads) continue;
+            const int64_t row = kv_row(P, slot, h);
+            const uint32_t wk = reinterpret_cast<const uint32_t*>(P.k)[row * LPR + l], wv = reinterpret_cast<const uint32_t*>(P.v)[row * LPR + l];
+            const float s_k = __half2float(P.ks[row * (LPR >> lg8) + (l >> lg8)]), s_v = __half2float(P.vs[row * (LPR >> lg8) + (l >> lg8)]);
+            const int64_t at = (slot.row * P.heads + h) * D + 8 * l;
+            *reinterpret_cast<uint4*>(k_out + at) = kv4_values(wk, s_k);
+            *reinterpret_cast<uint4*>(v_out + at) = kv4_values(wv, s_v);
+        }
     }
 }
 

@@ -61,7 +61,7 @@ int fmt_of(int bits, int group) {
 struct DeviceInfo {
     int checked = 0;  // 0 unknown, 1 supported, -1 not
     int sms = 0;
-    bool smem_set[64] = {};
+    bool smem_set[80] = {};
     // resident clusters per (format, cluster size, dynamic smem), queried once
     std::unordered_map<uint64_t, int> max_clusters;
 };
