@@ -425,7 +425,8 @@ wlq_status wlq_qk_norm_rope(const void* q, int64_t q_stride, int q_heads, const 
  * wlq_kv4_append: keys normed and rotated by wlq_qk_norm_rope's formula
  * (k_weight, positions NULL: neither), values as they are, both rounded to 4
  * bits and written to their places.  The codes and scales are exactly those of
- * the bf16 values nearest to the real keys.  k, v: bf16 with token strides.
+ * the real keys rounded to fp32 and from there to bf16.  k, v: bf16 with token
+ * strides.
  * A value beyond 65280 in magnitude, an infinity or a NaN sets
  * WLQ_ERR_NONFINITE; its group gets scale 0 and codes 0.  Pages that one call
  * writes must belong to one sequence.  batch * max_q < 2^31.

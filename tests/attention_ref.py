@@ -21,6 +21,11 @@ def bf16_rne(x: np.ndarray) -> np.ndarray:
         return np.where(np.isfinite(x), np.rint(x / step) * step, x)
 
 
+def key_bits(y: np.ndarray) -> np.ndarray:
+    """Real keys as the cache rounds them before their codes: to fp32, from there to bf16 (as fp64 values)."""
+    return bf16_rne(np.asarray(y).astype(np.float32).astype(np.float64))
+
+
 def norm_rope(x, weight, eps, positions, inv_freq, sections, interleaved):
     """x [T, H, D] fp64 -> the real-number result in fp64 (not rounded)."""
     x = np.array(x, dtype=np.float64)

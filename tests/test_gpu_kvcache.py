@@ -3,10 +3,10 @@
 qk_norm_rope evaluates in fp32, within E = 9 * 2^-24 r (|a| + |b|) of the real
 value y, and rounds once to bf16: the result lies between the bf16 values
 nearest to y - E and y + E, which is what is checked; nearly all equal the one
-nearest to y.  The cache promises the exact 4-bit rounding of the bf16 keys
-nearest to the real ones, so its codes are compared for equality: the 64-bit
-form is off by about 2^-49, and a bf16 border lies that close to a value with
-a chance of about 2^-40."""
+nearest to y.  The cache promises the exact 4-bit rounding of the real keys
+rounded to fp32 and then to bf16, so its codes are compared for equality: the
+64-bit form is off by about 2^-49, and a border lies that close to a value
+with a chance of about 2^-40."""
 import numpy as np
 import pytest
 import torch
@@ -152,7 +152,7 @@ def test_append_writes_the_exact_codes(D, group, page, heads, q_lens, kv_lens, r
     m.check_status()
     kr = ref.f64(k)
     if rotate:
-        kr = ref.bf16_rne(ref.norm_rope(kr, ref.f64(w), 1e-6, pos.numpy(), freq.numpy(), sections, rotate == 2))
+        kr = ref.key_bits(ref.norm_rope(kr, ref.f64(w), 1e-6, pos.numpy(), freq.numpy(), sections, rotate == 2))
     want = [t.cpu().numpy().copy() for t in before]
     for vals, ci, si in ((kr, 0, 1), (ref.f64(v), 2, 3)):
         q, s = ref.quantize4(vals, group)
@@ -180,13 +180,33 @@ def test_append_has_the_bits_of_quantize_ex_on_the_exact_keys():
     cu, kv, table = _dev(*_batch([T], [T], page, 1)[:3])
     cache = m.Kv4Cache(3, H, page, D, group)
     m.kv4_append(cache, x[:, :H], x[:, H:], cu, kv, table, T, pos, freq, k_weight=w)
-    exact = ref.bf16_rne(ref.norm_rope(ref.f64(x[:, :H]), ref.f64(w), 1e-6, pos.cpu().numpy(), freq.cpu().numpy(), (64,), True))
+    exact = ref.key_bits(ref.norm_rope(ref.f64(x[:, :H]), ref.f64(w), 1e-6, pos.cpu().numpy(), freq.cpu().numpy(), (64,), True))
     codes, scales = m.quantize_ex(torch.from_numpy(exact).bfloat16().cuda().reshape(T * H, D), 4, group, m.SCALE_F16)
     t = np.arange(T)
     pg = table.cpu().numpy()[0][t // page]
     got = cache[0].cpu().numpy()[pg, :, t % page]
     np.testing.assert_array_equal(ref.unpack4(got, D), codes.cpu().numpy().reshape(T, H, D))
     np.testing.assert_array_equal(cache[1].cpu().numpy()[pg, :, t % page], scales.cpu().numpy().reshape(T, H, -1))
+
+
+def test_append_of_many_rows_has_the_exact_codes():
+    """Enough keys (2 million) that values next to a border are among them: some 600 within fp32's error of one."""
+    m = wlq()
+    T, H, D, group, page = 1000, 16, 128, 128, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = (torch.randn(T, 2 * H, D, generator=g, device="cuda") * (1 + 3 * (torch.rand(D, generator=g, device="cuda") > 0.95))).bfloat16()
+    w = (1 + 0.2 * torch.randn(D, generator=g, device="cuda")).bfloat16()
+    pos, freq = _positions(3, T, 1, 1 << 20).cuda(), _freq((64,)).cuda()
+    cu, kv, table = _dev(*_batch([T], [T], page, 1)[:3])
+    cache = m.Kv4Cache(20, H, page, D, group)
+    for inter in (True, False):
+        m.kv4_append(cache, x[:, :H], x[:, H:], cu, kv, table, T, pos, freq, k_weight=w, interleaved=inter)
+        exact = ref.key_bits(ref.norm_rope(ref.f64(x[:, :H]), ref.f64(w), 1e-6, pos.cpu().numpy(), freq.cpu().numpy(), (64,), inter))
+        q, s = ref.quantize4(exact, group)
+        t = np.arange(T)
+        pg = table.cpu().numpy()[0][t // page]
+        np.testing.assert_array_equal(ref.unpack4(cache[0].cpu().numpy()[pg, :, t % page], D), q)
+        np.testing.assert_array_equal(cache[1].cpu().numpy()[pg, :, t % page].astype(np.float64), s)
 
 
 def test_append_flags_values_that_do_not_fit():

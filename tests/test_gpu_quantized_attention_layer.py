@@ -68,7 +68,7 @@ def test_prompt_then_single_tokens(group, sections, interleaved):
         # the same in 64 bits
         r = w8a8_64(ref.f64(x), qkv_q.cpu().double().numpy(), ref.f64(qkv_s).reshape(-1), ref.f64(bias)).reshape(T, Hq + 2 * Hk, D)
         rq = ref.bf16_rne(ref.norm_rope(r[:, :Hq], ref.f64(wq), 1e-6, pos, freq.numpy(), sections, interleaved))
-        rk = ref.bf16_rne(ref.norm_rope(r[:, Hq:Hq + Hk], ref.f64(wk), 1e-6, pos, freq.numpy(), sections, interleaved))
+        rk = ref.key_bits(ref.norm_rope(r[:, Hq:Hq + Hk], ref.f64(wk), 1e-6, pos, freq.numpy(), sections, interleaved))
         ro = np.zeros((T, Hq, D))
         for b in range(2):
             rows = slice(cu[b], cu[b + 1])

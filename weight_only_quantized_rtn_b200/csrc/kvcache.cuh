@@ -21,9 +21,10 @@
 // is exact (8 + 8 bits), and there are three more roundings; then it is
 // rounded to bf16.
 //
-// The cache's codes are those of the bf16 values nearest to the REAL keys: a
-// key on the other side of a border would change its code by a whole step, so
-// the append has to round as any exact evaluation does.  A value that can get
+// The cache's codes are those of the REAL keys rounded to fp32 and from there
+// to bf16 (as a cast from a wider type rounds): a key on the other side of a
+// border would change its code by a whole step, so the append has to round as
+// any exact evaluation does.  A value that can get
 // a code other than 0 (its magnitude is at least a 14th of its group's
 // largest) and has a bf16 midpoint within E, about one in three thousand, is
 // evaluated again in fp64 and rounded from there.  Doing so for every value
@@ -106,19 +107,6 @@ __device__ __forceinline__ void unpack8(uint4 u, float2 (&f)[4]) {
 
 __device__ __forceinline__ uint32_t bf16_rn_bits(float y) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(y));
-}
-
-// The bf16 value nearest to a double: the fp32 value nearest to it rounds the
-// same way unless it lies on a bf16 midpoint that the double does not; it is
-// then moved one unit towards the double.
-__device__ __noinline__ uint32_t bf16_from_f64(double y) {
-    float f = static_cast<float>(y);
-    if ((__float_as_uint(f) & 0xFFFFu) == 0x8000u) {
-        const double d = fabs(y) - fabs(static_cast<double>(f));
-        if (d > 0.0) f = __uint_as_float(__float_as_uint(f) + 1u);
-        else if (d < 0.0) f = __uint_as_float(__float_as_uint(f) - 1u);
-    }
-    return bf16_rn_bits(f);
 }
 
 // cos and sin of the token's angles for each pair, fp64 and rounded to fp32.
@@ -265,7 +253,7 @@ __device__ __forceinline__ bool settle_row(uint4 raw, bool norm, const RopeArgs&
                 c = t.x;
                 s = R.lo ? -t.y : t.y;
             }
-            const uint32_t b = bf16_from_f64((static_cast<double>(xi) * c + static_cast<double>(pi) * s) * r64);
+            const uint32_t b = bf16_rn_bits(static_cast<float>((static_cast<double>(xi) * c + static_cast<double>(pi) * s) * r64));
             o[i / 2] = (i & 1) ? ((o[i / 2] & 0xFFFFu) | (b << 16)) : ((o[i / 2] & 0xFFFF0000u) | b);
         }
     }
