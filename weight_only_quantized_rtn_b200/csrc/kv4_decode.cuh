@@ -23,9 +23,11 @@
 // powers of two), or E grows; most steps need one vote instead of a reduction
 // and a rescaling.
 //
-// Bound: HBM (each cached byte once); next to it the instruction issue, about
-// 480 instructions a warp for 32 tokens of D = 128, where HBM's rate leaves
-// 700.  A warp keeps three units of 32 tokens in a ring of its own in shared
+// Bound: HBM (each cached byte once); next to it the integer pipe, which
+// takes the codes apart (some 600 instructions a warp for 32 tokens of D = 128,
+// where HBM's rate leaves 700 issue slots).  Feeding K's stored nibbles without
+// their exact subtraction (the offsets' sum taken off the scores) left the
+// integer work as it is and was no faster.  A warp keeps two units of 32 tokens in a ring of its own in shared
 // memory (cp.async, 16-byte pieces permuted so that ldmatrix meets no bank
 // twice); 4 warps share a CTA's part of the sequence, and long sequences are
 // split over CTAs whose partial (M, l, O) kv4_combine_kernel joins in split
@@ -138,7 +140,7 @@ __device__ __forceinline__ void nibbles_codes(uint32_t w, uint32_t (&o)[4]) {
     o[3] = h2_bits(__hfma2(magic_pair(v, 0x00F000F0u), k16, k72));
 }
 
-constexpr int DEC_STAGES = 3;
+constexpr int DEC_STAGES = 2;  // three: 111 us against 109 for 64 ragged sequences, 78 against 73 for two long ones
 template <int D, int G>  // G groups a row
 struct DecRing {
     static constexpr int ROW = D / 2;                  // bytes of a row's codes
