@@ -124,6 +124,8 @@ DecPlan dec_plan(int64_t tokens, int batch, int max_q, int64_t max_kv, int q_hea
                  int sms) {
     DecPlan p;
     const int64_t rows = static_cast<int64_t>(max_q) * (q_heads / kv_heads);
+    // Up to 32 rows the few-row kernel, which reads the cache once for each 16 (8 sequences of 8192, 1 of 32768, 32 of
+    // 1500 tokens, D = 128: 45, 41, 44 us against 75, 43, 55 by the chunk kernel; 48 rows: 66, 53, 60 against 77, 44, 55).
     p.chunk = rows > 32;
     p.nt = rows > 8 ? 2 : 1;
     p.row_tiles = static_cast<int>(cdiv(rows, p.chunk ? 2 * wlq::CH_ROWS : 8 * p.nt));
@@ -374,6 +376,8 @@ struct I8Plan {
 I8Plan i8_plan(int64_t M, int64_t N, int64_t K) {
     I8Plan p;
     const int64_t KB = cdiv(K, 128);
+    // CTA pairs from half as many 256 x 256 tiles as there are pairs (48 tiles, 768 x 4096 x 4096: 13.5 us against 16.1 by
+    // single CTAs; 32 tiles, 512 x 4096 x 4096: 10.6 against 10.1)
     const int64_t pairs = kPlanSms / 2, nt2 = cdiv(N, 256), mt256 = cdiv(M, 256);
     if (nt2 * mt256 * 2 >= pairs) {
         // even token tiles: the count (a few from the least possible) whose rounds of tiles take the fewest columns
@@ -390,11 +394,16 @@ I8Plan i8_plan(int64_t M, int64_t N, int64_t K) {
         p.NT = static_cast<int>(nt2);
         p.b_bytes = static_cast<uint32_t>(p.bn / 2) * 128u;
     } else {
-        const int64_t t = cdiv(M, 128);
+        // Token tiles of 64 to 128: halved while that still leaves SMs without one (256 x 4096 x 4096: four of 64 take
+        // 8.8 us, two of 128 with K split in two 12.5).
+        int64_t t = cdiv(M, 128);
+        while (cdiv(N, 128) * t * 2 <= kPlanSms && cdiv(M, t) >= 128) t *= 2;
         p.bn = static_cast<int>(cdiv(cdiv(M, t), 16) * 16);
         p.NT = static_cast<int>(cdiv(N, 128));
         const int64_t tiles = p.NT * t;
-        while (p.S * 2 <= 8 && tiles * p.S * 2 <= kPlanSms && KB >= p.S * 2) p.S *= 2;
+        // K split over a cluster while SMs are idle; no more than 15 clusters of eight fit at once (96 x 2048 x 4096 with
+        // 16 of them: 12.6 us, a second round)
+        while (p.S * 2 <= 8 && tiles * p.S * 2 <= (p.S * 2 == 8 ? 120 : kPlanSms) && KB >= p.S * 2) p.S *= 2;
         p.b_bytes = static_cast<uint32_t>(p.bn) * 128u;
     }
     p.MT = static_cast<int>(cdiv(M, p.bn));
