@@ -389,6 +389,8 @@ wlq_status wlq_w4a4_linear(const void* x, int64_t M, const void* wq, const void*
  * inv_freq : fp32 [rotary_dim / 2]; sections: HOST int32 [axes]
  * q_out, k_out: bf16 with their own token strides; may be q and k themselves
  *          (same stride), otherwise they must not overlap any input
+ * With a weight, values beyond 1e18 in magnitude, whose squares leave fp32,
+ * are out of its range.
  * head_dim 64 or 128; rotary_dim a multiple of 16, at most head_dim; axes
  * 1..4; strides multiples of 8 and at least heads * head_dim; q, k, q_out and
  * k_out 16-byte aligned.  tokens == 0 is a no-op.
@@ -456,11 +458,13 @@ wlq_status wlq_kv4_read(const int32_t* cu_seqlens, const int32_t* kv_lens, int b
  * all of them (causal 0), j <= p (causal 1), p - window < j <= p (causal 1,
  * window > 0).  Query head h reads cache head h / (q_heads / kv_heads).
  * A query that sees nothing gets zeros (lse -inf).
- * q   : bf16, token strides as above; out: bf16 [tokens, q_heads, head_dim]
+ * q   : bf16, token strides as above; out: bf16 [tokens, q_heads, head_dim],
+ *       not overlapping q.  Cached scales are those the append writes (at most
+ *       9328: seven of them stay finite in fp16).
  * lse : fp32 [tokens, q_heads], log sum_j exp(scale q . k_j), or NULL
  * max_kv: an upper bound of kv_lens (host).  It only plans how long caches are
- *         split; any value gives right results.  The tokens of a page out of
- *         range count as not seen (WLQ_ERR_INDEX is set).
+ *         split; any value gives right results.  Tokens of a page out of range
+ *         and tokens past the table count as not seen (WLQ_ERR_INDEX is set).
  * scale: finite, any sign.  Scores, softmax statistics and sums are fp32, the
  * inputs of the tensor cores fp16, each rounded once: queries as q 2^e with one
  * power of two per row (exact unless a value lies 2^-29 below its row's
@@ -492,7 +496,7 @@ wlq_status wlq_kv4_attention(const void* q, int64_t q_stride, int64_t tokens, in
  * wq, ws: int8 [N, K] codes and fp32 [N] scales (wlq_quantize, bits 8, group 0)
  * bias  : bf16 [N] or NULL; y: [M, N] in y_dtype
  * K % 16 == 0, K <= 131056 (the sum fits 32 bits for any int8 codes); xq and
- * wq 16-byte aligned.  M == 0 or N == 0 is a no-op.
+ * wq 16-byte aligned, xs, ws and y 4-byte.  M == 0 or N == 0 is a no-op.
  */
 wlq_status wlq_int8_linear(const void* xq, const float* xs, int64_t M, const void* wq, const float* ws, int64_t N,
                            int64_t K, const void* bias, void* y, int y_dtype, void* stream);

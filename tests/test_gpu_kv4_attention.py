@@ -245,3 +245,64 @@ def test_streams_and_graphs():
     dev[1].fill_(64)  # the lengths are read when the graph runs
     g1.replay()
     assert torch.equal(o1, m.kv4_attention(q, cache, *dev, 1, 3000))
+
+
+def test_lengths_past_the_table_end_at_once():
+    """A length the table has no room for (up to 2^31 - 1): its tokens count as not seen, and nobody walks them."""
+    m = wlq()
+    for n in (1, 50):
+        q, cache, cu, kv, table = make(6, [n, 1], [64, 40], 1, 2, 64, 32, 16)
+        dev = [torch.from_numpy(x).cuda() for x in (cu, kv, table)]
+        want = m.kv4_attention(q, cache, *dev, n, 64, causal=False)
+        dev[1][0] = (1 << 31) - 1
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        got = m.kv4_attention(q, cache, *dev, n, 64, causal=False)
+        end.record()
+        assert m.get_status() == m.ERR_INDEX
+        assert torch.equal(got, want)  # not causal: all of the table's tokens
+        assert start.elapsed_time(end) < 100
+        dev[1][0] = 0
+    m.check_status()
+
+
+def test_calls_on_a_given_stream():
+    m = wlq()
+    q, cache, cu, kv, table = make(8, [1, 1], [3000, 500], 2, 4, 128, 64, 64)
+    dev = [torch.from_numpy(x).cuda() for x in (cu, kv, table)]
+    want = m.kv4_attention(q, cache, *dev, 1, 3000)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = [m.kv4_attention(q, cache, *dev, 1, 3000, stream=s) for _ in range(20)]
+    junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(20)]  # may not take the calls' workspaces
+    s.synchronize()
+    assert all(torch.equal(o, want) for o in got) and len(junk) == 20
+
+
+def test_tensors_elsewhere_and_of_other_shapes_are_refused():
+    m = wlq()
+    q, cache, cu, kv, table = make(8, [1], [30], 2, 4, 64, 32, 16)
+    dev = [torch.from_numpy(x).cuda() for x in (cu, kv, table)]
+    bad = [
+        (q.cpu(), cache, *dev), (q.float(), cache, *dev), (q[0], cache, *dev), (q[:, :, :32], cache, *dev), (q[:, :3], cache, *dev),
+        (q, (cache[0].cpu(),) + tuple(cache[1:]), *dev), (q, (cache[0], cache[1].float()) + tuple(cache[2:]), *dev),
+        (q, (cache[0][..., :16], *cache[1:]), *dev), (q, cache, dev[0].long(), dev[1], dev[2]), (q, cache, dev[0][:1], dev[1], dev[2]),
+        (q, cache, dev[0], dev[1], dev[2][0]), (q.transpose(1, 2).contiguous().transpose(1, 2), cache, *dev),
+    ]
+    for args in bad:
+        with pytest.raises(m.WlqError):
+            m.kv4_attention(*args, 1, 30)
+    with pytest.raises(m.WlqError):
+        m.kv4_attention(q, cache, *dev, 1, 30, out=torch.empty_like(q).float())
+    with pytest.raises(m.WlqError):
+        m.kv4_attention(q, cache, *dev, 1, 30, lse=torch.empty(1, 8, device="cuda").half())
+    with pytest.raises(m.WlqError):
+        m.qk_norm_rope(q, None, torch.zeros(2, dtype=torch.int32, device="cuda"), torch.ones(32, device="cuda"))
+    with pytest.raises(m.WlqError):
+        m.qk_norm_rope(q, None, torch.zeros(1, dtype=torch.int32, device="cuda"))
+    with pytest.raises(m.WlqError):
+        m.qk_norm_rope(None, None)
+    with pytest.raises(m.WlqError):
+        m.w8a8_linear(torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(8, 32, dtype=torch.int8, device="cuda"), torch.ones(8, device="cuda"))
+    with pytest.raises(m.WlqError):
+        m.w8a8_linear(torch.zeros(2, 24, dtype=torch.bfloat16, device="cuda"), torch.zeros(8, 24, dtype=torch.int8, device="cuda"), torch.ones(8, device="cuda"))

@@ -14,6 +14,7 @@ SRC = """
 extern "C" int seq(long long r0, long long r1, long long kv, long long mq, long long t) { return wlq::kv_sequence(r0, r1, kv, mq, t); }
 extern "C" int entry(long long pos, long long w, int sh, long long* e, int* p) {
     int64_t x; int r = wlq::kv_entry(pos, w, sh, &x, p); *e = x; return r; }
+extern "C" int covered(long long kv, long long w, int sh) { return wlq::kv_covered(kv, w, sh); }
 extern "C" int page_ok(long long p, long long n) { return wlq::kv_page_ok(p, n); }
 """
 
@@ -28,6 +29,7 @@ def rules(tmp_path_factory):
     L.seq.argtypes = [i64] * 5
     L.entry.argtypes = [i64, i64, ctypes.c_int, ctypes.POINTER(i64), ctypes.POINTER(ctypes.c_int)]
     L.page_ok.argtypes = [i64, i64]
+    L.covered.argtypes = [i64, i64, ctypes.c_int]
     return L
 
 
@@ -56,3 +58,11 @@ def test_pages(rules):
     for page in (-(1 << 31), -1, 0, 1, 4, 5, (1 << 31) - 1):
         for n in (0, 1, 5):
             assert bool(rules.page_ok(page, n)) == (0 <= page < n)
+
+
+def test_covered_tokens(rules):
+    for kv in (-1, 0, 1, 16, 47, 48, 49, (1 << 31) - 1):
+        for width in (0, 1, 3, 1 << 24, 1 << 40):
+            for shift in (4, 8):
+                want = max(0, min(kv, width << shift))
+                assert rules.covered(kv, width, shift) == want

@@ -346,6 +346,8 @@ def _on(*tensors):
 
 def _head_rows(name: str, x, head_dim: int):
     """(pointer, token stride, heads) of bf16 x [tokens, heads, head_dim], heads contiguous within a token."""
+    if x.dim() != 3:
+        raise WlqError(ERR_INVALID_ARG, name + " must be [tokens, heads, head_dim]")
     T, H, D = x.shape
     st, sh, sd = x.stride()
     if x.dtype is not torch.bfloat16:
@@ -396,8 +398,12 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, sections=None, interleaved
     positions int32 [tokens] or [tokens, axes], inv_freq fp32 [rotary_dim / 2],
     sections: the pairs that turn by each axis.  interleaved: pairs (2 i,
     2 i + 1), else (i, i + rotary_dim / 2).  q_out / k_out may be q / k."""
+    if stream is not None:  # what is allocated here belongs to that stream, too
+        with torch.cuda.stream(stream):
+            return qk_norm_rope(q, k, positions, inv_freq, sections, interleaved, q_weight, k_weight, eps, q_out, k_out)
     some = q if q is not None else k
     _want(some is not None, "q or k is needed")
+    _want(some.dim() == 3, "q and k must be [tokens, heads, head_dim]")
     T, _, D = some.shape
     _on(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
     qp = kp = qo = ko = None
@@ -421,16 +427,17 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, sections=None, interleaved
             ko, kos, _ = _head_rows("k_out", k_out, D)
     _check(lib.wlq_qk_norm_rope(qp, qs, hq, kp, ks, hk, T, D, _weight("q_weight", q_weight, D),
                                 _weight("k_weight", k_weight, D), eps, *_rope(positions, inv_freq, sections, T),
-                                int(interleaved), qo, qos, ko, kos, _stream(stream)))
+                                int(interleaved), qo, qos, ko, kos, _stream()))
     return q_out, k_out
 
 
 def _pool(cache):
     """(pointers..., num_pages, page_size, group), heads, head_dim of a 4-bit cache."""
     kc, ks, vc, vs = cache
-    shape = kc.shape
+    shape, scales = kc.shape, ks.shape
+    if len(shape) != 4 or len(scales) != 4:
+        raise WlqError(ERR_INVALID_ARG, "cache: four arrays of four dimensions")
     pages, H, P, half = shape
-    scales = ks.shape
     groups = scales[3]
     if (kc.dtype is not torch.uint8 or vc.dtype is not torch.uint8 or ks.dtype is not torch.float16 or vs.dtype is not torch.float16
             or vc.shape != shape or vs.shape != scales or scales != (pages, H, P, groups) or groups == 0):
@@ -442,6 +449,8 @@ def _pool(cache):
 
 
 def _batch(cu_seqlens, kv_lens, block_table, max_q: int):
+    if block_table.dim() != 2:
+        raise WlqError(ERR_INVALID_ARG, "block_table must be [batch, width]")
     n, width = block_table.shape
     i32 = torch.int32
     if (cu_seqlens.dtype is not i32 or kv_lens.dtype is not i32 or block_table.dtype is not i32 or cu_seqlens.numel() != n + 1
@@ -457,6 +466,9 @@ def kv4_append(cache, k, v, cu_seqlens, kv_lens, block_table, max_q: int, positi
     free.  Sequence b's tokens cu_seqlens[b] .. cu_seqlens[b + 1] become the
     last of its kv_lens[b] cached ones, on pages block_table[b]; max_q: an upper
     bound of the sequences' token counts."""
+    if stream is not None:  # what is allocated here belongs to that stream, too
+        with torch.cuda.stream(stream):
+            return kv4_append(cache, k, v, cu_seqlens, kv_lens, block_table, max_q, positions, inv_freq, sections, interleaved, k_weight, eps)
     ptrs, H, D = _pool(cache)
     T = k.shape[0]
     _on(k, v, *cache, cu_seqlens, kv_lens, block_table, positions, inv_freq, k_weight)
@@ -466,18 +478,21 @@ def kv4_append(cache, k, v, cu_seqlens, kv_lens, block_table, max_q: int, positi
         raise WlqError(ERR_INVALID_ARG, "k and v must be [tokens, the cache's heads, head_dim]")
     _check(lib.wlq_kv4_append(kp, kst, vp, vst, T, H, D, _weight("k_weight", k_weight, D), eps,
                               *_rope(positions, inv_freq, sections, T), int(interleaved),
-                              *_batch(cu_seqlens, kv_lens, block_table, max_q), *ptrs, _stream(stream)))
+                              *_batch(cu_seqlens, kv_lens, block_table, max_q), *ptrs, _stream()))
 
 
 def kv4_read(cache, cu_seqlens, kv_lens, block_table, max_q: int, tokens: int, stream=None):
     """The cached rows of the call's tokens as bf16 -> (k, v) [tokens, heads,
     head_dim] (rows of no sequence stay uninitialised)."""
+    if stream is not None:  # what is allocated here belongs to that stream, too
+        with torch.cuda.stream(stream):
+            return kv4_read(cache, cu_seqlens, kv_lens, block_table, max_q, tokens)
     ptrs, H, D = _pool(cache)
     _on(*cache, cu_seqlens, kv_lens, block_table)
     k = torch.empty((tokens, H, D), dtype=torch.bfloat16, device=cache[0].device)
     v = torch.empty_like(k)
     _check(lib.wlq_kv4_read(*_batch(cu_seqlens, kv_lens, block_table, max_q), *ptrs, tokens, H, D, k.data_ptr(),
-                            v.data_ptr(), _stream(stream)))
+                            v.data_ptr(), _stream()))
     return k, v
 
 
@@ -498,9 +513,12 @@ def kv4_attention(q, cache, cu_seqlens, kv_lens, block_table, max_q: int, max_kv
     default.  lse: fp32 [tokens, q_heads] to be filled, or None.  Rows of no
     sequence are left as they were (uninitialised without out).  workspace: of
     kv4_attention_workspace bytes; allocated here if None."""
+    if stream is not None:  # what is allocated here belongs to that stream, too
+        with torch.cuda.stream(stream):
+            return kv4_attention(q, cache, cu_seqlens, kv_lens, block_table, max_q, max_kv, scale, causal, window, out, lse, workspace)
     ptrs, H, D = _pool(cache)
-    T, Hq, Dq = q.shape
-    _want(Dq == D, "q needs the cache's head_dim")
+    _want(q.dim() == 3 and q.shape[2] == D, "q must be [tokens, q_heads, the cache's head_dim]")
+    T, Hq, _ = q.shape
     _on(q, *cache, cu_seqlens, kv_lens, block_table, out, lse, workspace)
     qp, qs, _ = _head_rows("q", q, D)
     if out is None:
@@ -517,7 +535,7 @@ def kv4_attention(q, cache, cu_seqlens, kv_lens, block_table, max_q: int, max_kv
     _check(lib.wlq_kv4_attention(qp, qs, T, Hq, H, D, batch[0], batch[1], batch[2], batch[3], max_kv, batch[4], batch[5], *ptrs,
                                  D ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(),
                                  None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), ws_n,
-                                 _stream(stream)))
+                                 _stream()))
     return out
 
 
@@ -538,13 +556,17 @@ def _int8_operands(y, wq, ws, bias, M: int, K: int):
 def int8_linear_into(y, xq, xs, wq, ws, bias=None, stream=None):
     """y = xs ws (xq wq^T) + b from int8 codes xq [M, K], wq [N, K] and fp32 scales of
     each token and output channel (quantize_ex(x, 8, 0), quantize(W, 8, 0)); y bf16 or fp32."""
+    if stream is not None:  # what is allocated here belongs to that stream, too
+        with torch.cuda.stream(stream):
+            return int8_linear_into(y, xq, xs, wq, ws, bias)
+    _want(xq.dim() == 2 and wq.dim() == 2, "xq and wq must be [M, K] and [N, K]")
     M, K = xq.shape
     _on(y, xq, xs, wq, ws, bias)
     _want(xq.dtype == torch.int8 and xq.is_contiguous(), "xq must be contiguous int8 [M, K]")
     _want(xs.dtype == torch.float32 and xs.numel() == M and xs.is_contiguous(), "xs must be contiguous fp32 [M]")
     N, out = _int8_operands(y, wq, ws, bias, M, K)
     _check(lib.wlq_int8_linear(xq.data_ptr(), xs.data_ptr(), M, wq.data_ptr(), ws.data_ptr(), N, K,
-                               None if bias is None else bias.data_ptr(), y.data_ptr(), out, _stream(stream)))
+                               None if bias is None else bias.data_ptr(), y.data_ptr(), out, _stream()))
     return y
 
 
@@ -556,6 +578,10 @@ def w8a8_workspace(M: int, K: int) -> int:
 def w8a8_linear_into(y, x, wq, ws, bias=None, workspace=None, stream=None):
     """The W8A8 forward from bf16 x [M, K]: x quantized token by token in the
     workspace, then y = xs ws (xq wq^T) + b (int8 wq [N, K], fp32 ws [N])."""
+    if stream is not None:  # what is allocated here belongs to that stream, too
+        with torch.cuda.stream(stream):
+            return w8a8_linear_into(y, x, wq, ws, bias, workspace)
+    _want(x.dim() == 2 and wq.dim() == 2, "x and wq must be [M, K] and [N, K]")
     M, K = x.shape
     _on(y, x, wq, ws, bias, workspace)
     _want(x.dtype == torch.bfloat16 and x.is_contiguous(), "x must be contiguous bf16 [M, K]")
@@ -565,14 +591,17 @@ def w8a8_linear_into(y, x, wq, ws, bias=None, workspace=None, stream=None):
         workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
     ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.wlq_w8a8_linear(x.data_ptr(), M, wq.data_ptr(), ws.data_ptr(), N, K, None if bias is None else bias.data_ptr(),
-                               y.data_ptr(), out, None if workspace is None else workspace.data_ptr(), ws_n, _stream(stream)))
+                               y.data_ptr(), out, None if workspace is None else workspace.data_ptr(), ws_n, _stream()))
     return y
 
 
 def w8a8_linear(x, wq, ws, bias=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
     """w8a8_linear_into with a new y [M, N]."""
+    if stream is not None:  # what is allocated here belongs to that stream, too
+        with torch.cuda.stream(stream):
+            return w8a8_linear(x, wq, ws, bias, out_dtype, workspace)
     y = torch.empty((x.shape[0], wq.shape[0]), dtype=out_dtype, device=x.device)
-    return w8a8_linear_into(y, x, wq, ws, bias, workspace, stream)
+    return w8a8_linear_into(y, x, wq, ws, bias, workspace)
 
 
 def get_status(stream=None) -> int:

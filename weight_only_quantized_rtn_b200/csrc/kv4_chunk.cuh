@@ -133,6 +133,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
         if (seq == KV_BAD && threadIdx.x == 0) raise_error(ERRBIT_INDEX);
         return;
     }
+    const int cover = kv_covered(kv, a.B.table_stride, a.P.page_shift);
+    if (cover < kv && threadIdx.x == 0) raise_error(ERRBIT_INDEX);
     const int n = static_cast<int>(r1 - r0), rows = n * a.share, row0 = rt * 2 * CH_ROWS;
     if (row0 >= rows) return;
 
@@ -142,7 +144,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
         int lo, hi, unused;
         seen_range(a, kv - n + row0 / a.share, kv, lo, unused);
         seen_range(a, kv - n + (min(rows, row0 + 2 * CH_ROWS) - 1) / a.share, kv, unused, hi);
-        const int u0 = lo / CH_KEYS, u1 = (hi + CH_KEYS - 1) / CH_KEYS, units = max(0, u1 - u0);
+        hi = min(hi, cover);
+        const int u0 = lo / CH_KEYS, u1 = hi > 0 ? (hi - 1) / CH_KEYS + 1 : 0, units = max(0, u1 - u0);
         j0 = u0 + static_cast<int>(static_cast<int64_t>(units) * split / a.splits);
         j1 = u0 + static_cast<int>(static_cast<int64_t>(units) * (split + 1) / a.splits);
 #pragma unroll
@@ -153,7 +156,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
                 seen_range(a, kv - n + f / a.share, kv, lo, unused);
                 seen_range(a, kv - n + l / a.share, kv, unused, hi);
                 R[t].jb = max(j0, lo / CH_KEYS);
-                R[t].je = max(R[t].jb, min(j1, (hi + CH_KEYS - 1) / CH_KEYS));
+                hi = min(hi, cover);
+                R[t].je = max(R[t].jb, min(j1, hi > 0 ? (hi - 1) / CH_KEYS + 1 : 0));
             }
         }
     }

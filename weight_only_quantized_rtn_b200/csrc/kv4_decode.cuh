@@ -255,6 +255,8 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
         if (seq == KV_BAD && threadIdx.x == 0) raise_error(ERRBIT_INDEX);
         return;
     }
+    const int cover = kv_covered(kv, a.B.table_stride, a.P.page_shift);
+    if (cover < kv && threadIdx.x == 0) raise_error(ERRBIT_INDEX);
     const int n = static_cast<int>(r1 - r0), rows = n * a.share, row0 = rt * 8 * NT;
     if (row0 >= rows) return;
     const int row_last = min(rows, row0 + 8 * NT) - 1;
@@ -262,7 +264,8 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
     int lo, hi, lo_all, hi_all;
     seen_range(a, kv - n + row0 / a.share, kv, lo, hi_all);
     seen_range(a, kv - n + row_last / a.share, kv, lo_all, hi);
-    const int u0 = lo / DEC_UNIT, u1 = (hi + DEC_UNIT - 1) / DEC_UNIT, units = max(0, u1 - u0);
+    hi = min(hi, cover);
+    const int u0 = lo / DEC_UNIT, u1 = hi > 0 ? (hi - 1) / DEC_UNIT + 1 : 0, units = max(0, u1 - u0);
     const int ub = u0 + static_cast<int>(static_cast<int64_t>(units) * split / a.splits);
     const int ue = u0 + static_cast<int>(static_cast<int64_t>(units) * (split + 1) / a.splits);
 

@@ -29,6 +29,14 @@ WLQ_HD KvRange kv_entry(int64_t pos, int64_t table_width, int shift, int64_t* en
     return pos >= 0 && *entry < table_width ? KV_OK : KV_BAD;
 }
 
+// How many cached tokens a call looks at: those the table has room for (a
+// length beyond it is out of range; nothing is gained by walking it).
+WLQ_HD int kv_covered(int64_t kv_len, int64_t table_width, int shift) {
+    const int64_t room = table_width >= (int64_t(1) << 31) ? (int64_t(1) << 31) - 1 : table_width << shift;
+    const int64_t n = kv_len < room ? kv_len : room;
+    return static_cast<int>(n < 0 ? 0 : n);
+}
+
 WLQ_HD bool kv_page_ok(int64_t page, int64_t pages) { return page >= 0 && page < pages; }
 
 }  // namespace wlq
