@@ -35,7 +35,9 @@
 // lanes hold it, 8 adjacent values each (one 16-byte load), so the norm is a
 // shuffle reduction and the half-split partner one shuffle.  A CTA works out
 // its token's angles once, in fp64, and walks the token's heads with cos and
-// sin in registers.
+// sin in registers.  Measured for 6240 tokens: norm + rotation of 64 heads 45 us
+// (205 MB: 0.69 of the copy rate; issue 66 % active), append of 32 heads 73 us
+// (120 MB; issue 73 % active: the exact rounding), read back 28 us (122 MB).
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
