@@ -530,7 +530,7 @@ def kv4_attention(q, cache, cu_seqlens, kv_lens, block_table, max_q: int, max_kv
     batch = _batch(cu_seqlens, kv_lens, block_table, max_q)
     if workspace is None:
         n = int(lib.wlq_kv4_attention_workspace(T, batch[2], batch[3], max_kv, Hq, H, D))
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        workspace = out.new_empty((n + 1) // 2) if n else None  # bf16: two bytes each
     ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.wlq_kv4_attention(qp, qs, T, Hq, H, D, batch[0], batch[1], batch[2], batch[3], max_kv, batch[4], batch[5], *ptrs,
                                  D ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(),
@@ -588,7 +588,7 @@ def w8a8_linear_into(y, x, wq, ws, bias=None, workspace=None, stream=None):
     N, out = _int8_operands(y, wq, ws, bias, M, K)
     if workspace is None:
         n = int(lib.wlq_w8a8_workspace(M, K))
-        workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+        workspace = x.new_empty((n + 1) // 2) if n else None  # bf16: two bytes each
     ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.wlq_w8a8_linear(x.data_ptr(), M, wq.data_ptr(), ws.data_ptr(), N, K, None if bias is None else bias.data_ptr(),
                                y.data_ptr(), out, None if workspace is None else workspace.data_ptr(), ws_n, _stream()))

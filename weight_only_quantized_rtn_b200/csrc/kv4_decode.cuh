@@ -26,7 +26,9 @@
 // A warp keeps two units of 32 tokens in a ring of its own in shared memory
 // (cp.async, 16-byte pieces permuted so that ldmatrix meets no bank twice); 4
 // warps share a CTA's part of the sequence, and long sequences are split over
-// CTAs whose partial (M, l, O) kv4_combine_kernel joins in split order.
+// CTAs whose partial (M, l, O) are joined in split order: up to eight short
+// parts by their cluster through distributed shared memory, others by
+// kv4_combine_kernel.
 //
 // Bound: HBM (each cached byte once); next to it the integer pipe, which takes
 // the codes apart (some 600 instructions a warp for 32 tokens of D = 128, where
@@ -62,6 +64,7 @@ struct AttnArgs {
     float* part_o;   // [tokens * q_heads][splits][D]
     float2* part_ml;  // [tokens * q_heads][splits]: (m, l)
     int splits, row_tiles;
+    int cluster;  // the splits are the CTAs of a cluster, which joins their parts itself
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -544,6 +547,13 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
             }
         }
     __syncthreads();
+    const bool join = a.cluster != 0;
+    auto finish = [&](int r, int d, float2 v, float M, float L) {  // inputs d, d + 1 of row r's result
+        const int64_t head_row = (r0 + (row0 + r) / a.share) * a.q_heads + h * a.share + (row0 + r) % a.share;
+        const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);  // a NaN stays one
+        *reinterpret_cast<__nv_bfloat162*>(a.out + head_row * D + d) = __floats2bfloat162_rn(v.x * inv, v.y * inv);
+        if (d == 0 && a.lse) a.lse[head_row] = L > 0.0f ? (M + __log2f(L)) * 0.6931471805599453f : (L == 0.0f ? -INFINITY : L);
+    };
     for (int r = warp; r < 8 * NT && row0 + r < rows; r += DEC_WARPS) {
         float M = -INFINITY, L = 0.0f, w[DEC_WARPS];
 #pragma unroll
@@ -553,8 +563,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
             w[i] = M == -INFINITY ? 0.0f : ex2(sm_ml[i * 8 * NT + r].x - M);
             L += w[i] * sm_ml[i * 8 * NT + r].y;
         }
-        const int64_t head_row = (r0 + (row0 + r) / a.share) * a.q_heads + h * a.share + (row0 + r) % a.share;
-        const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);  // a NaN stays one
+        const int64_t part = ((r0 + (row0 + r) / a.share) * a.q_heads + h * a.share + (row0 + r) % a.share) * a.splits + split;
 #pragma unroll
         for (int d = 2 * lane; d < D; d += 64) {
             float2 v = make_float2(0.0f, 0.0f);
@@ -564,17 +573,37 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
                 v.x += w[i] * y.x;
                 v.y += w[i] * y.y;
             }
-            if (a.splits == 1) {
-                const __nv_bfloat162 y = __floats2bfloat162_rn(v.x * inv, v.y * inv);
-                *reinterpret_cast<__nv_bfloat162*>(a.out + head_row * D + d) = y;
-            } else {
-                *reinterpret_cast<float2*>(a.part_o + (head_row * a.splits + split) * D + d) = v;
+            if (a.splits == 1) finish(r, d, v, M, L);
+            else if (join) *reinterpret_cast<float2*>(sm_o + r * (D + 4) + d) = v;  // over warp 0's part, which this lane has read
+            else *reinterpret_cast<float2*>(a.part_o + part * D + d) = v;
+        }
+        __syncwarp();
+        if (lane == 0 && a.splits > 1) (join ? sm_ml[r] : a.part_ml[part]) = make_float2(M, L);
+    }
+    if (join) {
+        // the cluster's parts, in order: a warp for each row
+        cluster_sync_all();
+        const uint32_t o_at = smem_u32(sm_o), ml_at = smem_u32(sm_ml);
+        for (int r = split * DEC_WARPS + warp; r < 8 * NT && row0 + r < rows; r += a.splits * DEC_WARPS) {
+            float M = -INFINITY, L = 0.0f;
+            for (int i = 0; i < a.splits; ++i) M = fmaxf(M, ld_dsmem_f32(mapa_shared(ml_at + r * 8, i)));
+            float2 v[D / 64];
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) v[k] = make_float2(0.0f, 0.0f);
+            for (int i = 0; i < a.splits; ++i) {
+                const uint32_t ml = mapa_shared(ml_at + r * 8, i), o = mapa_shared(o_at + r * (D + 4) * 4, i);
+                const float w = M == -INFINITY ? 0.0f : ex2(ld_dsmem_f32(ml) - M);
+                L += w * ld_dsmem_f32(ml + 4);
+#pragma unroll
+                for (int k = 0; k < D / 64; ++k) {
+                    v[k].x += w * ld_dsmem_f32(o + (2 * lane + 64 * k) * 4);
+                    v[k].y += w * ld_dsmem_f32(o + (2 * lane + 64 * k) * 4 + 4);
+                }
             }
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) finish(r, 2 * lane + 64 * k, v[k], M, L);
         }
-        if (lane == 0) {
-            if (a.splits > 1) a.part_ml[head_row * a.splits + split] = make_float2(M, L);
-            else if (a.lse) a.lse[head_row] = L > 0.0f ? (M + __log2f(L)) * 0.6931471805599453f : (L == 0.0f ? -INFINITY : L);
-        }
+        cluster_sync_all();  // no CTA leaves while its part is being read
     }
 }
 
