@@ -134,6 +134,23 @@ def test_long_caches_are_split(kv, window):
     m.check_status()
 
 
+@pytest.mark.parametrize("D,group,page", [(128, 64, 64), (64, 32, 16)])
+@pytest.mark.parametrize("share,max_q", [(4, 1), (3, 4), (8, 4)])
+@pytest.mark.parametrize("longest", [600, 799, 1100, 1400, 1800, 2100])
+def test_parts_joined_without_a_workspace(D, group, page, share, max_q, longest):
+    """Two to eight short parts a sequence: some hold nothing (short and empty sequences, a window, bad pages)."""
+    m = wlq()
+    a = make(longest, [1, max_q, max_q - 1, 1, max_q], [longest, longest - 37, max_q - 1, 33, longest // 2], 2, share, D, group, page)
+    assert m.kv4_attention_workspace(a[0].shape[0], 5, max_q, longest, 2 * share, 2, D) == 0
+    for causal, window in ((True, 0), (False, 0), (True, 50)):
+        check(m, *a, 2, causal, window)
+    m.check_status()
+    a[4][1, 2:-1] = -1
+    check(m, *a, 2, True, 0, random=False)
+    assert m.get_status() == m.ERR_INDEX
+    m.check_status()
+
+
 def test_scores_that_grow_move_the_maximum():
     """Keys whose scores climb by far more than the lazy maximum's 2^8, then fall; the largest last, first and in between."""
     m = wlq()
