@@ -150,3 +150,12 @@ def test_w8a8_refuses(want, kw):
 def test_int8_of_nothing_is_a_no_op():
     assert int8(M=0) == m.OK and int8(N=0) == m.OK and w8a8(M=0) == m.OK and w8a8(N=0) == m.OK
     assert m.w8a8_workspace(4, 128) >= 4 * 128 + 16 and m.w8a8_workspace(0, 128) == 0 and m.w8a8_workspace(4, 24) == 0
+
+
+def test_caches_copy_and_save():
+    import copy
+    import pickle
+
+    cache = m.Kv4Cache(3, 2, 16, 64, 32, device="cpu")
+    for again in (copy.copy(cache), copy.deepcopy(cache), pickle.loads(pickle.dumps(cache))):
+        assert [(t.shape, t.dtype) for t in again] == [(t.shape, t.dtype) for t in cache]

@@ -323,3 +323,17 @@ def test_tensors_elsewhere_and_of_other_shapes_are_refused():
         m.w8a8_linear(torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(8, 32, dtype=torch.int8, device="cuda"), torch.ones(8, device="cuda"))
     with pytest.raises(m.WlqError):
         m.w8a8_linear(torch.zeros(2, 24, dtype=torch.bfloat16, device="cuda"), torch.zeros(8, 24, dtype=torch.int8, device="cuda"), torch.ones(8, device="cuda"))
+
+
+def test_workspaces_that_are_views_of_less_memory_are_refused():
+    m = wlq()
+    q, cache, cu, kv, table = make(8, [1, 1], [30, 20], 2, 4, 64, 32, 16)
+    dev = [torch.from_numpy(x).cuda() for x in (cu, kv, table)]
+    n = m.kv4_attention_workspace(2, 2, 1, 1 << 20, 8, 2, 64)
+    assert n > 0
+    ws = torch.empty(1, dtype=torch.uint8, device="cuda").expand(n)
+    with pytest.raises(m.WlqError, match="contiguous"):
+        m.kv4_attention(q, cache, *dev, 1, 1 << 20, workspace=ws)
+    x, wq, s = torch.zeros(4, 128, device="cuda").bfloat16(), torch.zeros(16, 128, dtype=torch.int8, device="cuda"), torch.ones(16, device="cuda")
+    with pytest.raises(m.WlqError, match="contiguous"):
+        m.w8a8_linear(x, wq, s, workspace=torch.empty(1, dtype=torch.uint8, device="cuda").expand(m.w8a8_workspace(4, 128)))

@@ -330,6 +330,9 @@ class Kv4Cache(tuple):
         return super().__new__(cls, (torch.zeros((num_pages, heads, page_size, n), dtype=t, device=device)
                                      for n, t in shapes))
 
+    def __reduce__(self):  # copies and saved caches are plain tuples
+        return tuple, (tuple(self),)
+
 
 def _want(ok: bool, what: str):
     if not ok:
@@ -342,6 +345,13 @@ def _on(*tensors):
     for t in tensors:
         if t is not None and t.get_device() != cur:  # -1 on the host
             raise WlqError(ERR_INVALID_ARG, "tensors must be on the current CUDA device (cuda:%d)" % cur)
+
+
+def _ws_bytes(workspace) -> int:
+    if workspace is None:
+        return 0
+    _want(workspace.is_contiguous(), "workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
 
 
 def _head_rows(name: str, x, head_dim: int):
@@ -531,7 +541,7 @@ def kv4_attention(q, cache, cu_seqlens, kv_lens, block_table, max_q: int, max_kv
     if workspace is None:
         n = int(lib.wlq_kv4_attention_workspace(T, batch[2], batch[3], max_kv, Hq, H, D))
         workspace = out.new_empty((n + 1) // 2) if n else None  # bf16: two bytes each
-    ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_n = _ws_bytes(workspace)
     _check(lib.wlq_kv4_attention(qp, qs, T, Hq, H, D, batch[0], batch[1], batch[2], batch[3], max_kv, batch[4], batch[5], *ptrs,
                                  D ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(),
                                  None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), ws_n,
@@ -589,7 +599,7 @@ def w8a8_linear_into(y, x, wq, ws, bias=None, workspace=None, stream=None):
     if workspace is None:
         n = int(lib.wlq_w8a8_workspace(M, K))
         workspace = x.new_empty((n + 1) // 2) if n else None  # bf16: two bytes each
-    ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_n = _ws_bytes(workspace)
     _check(lib.wlq_w8a8_linear(x.data_ptr(), M, wq.data_ptr(), ws.data_ptr(), N, K, None if bias is None else bias.data_ptr(),
                                y.data_ptr(), out, None if workspace is None else workspace.data_ptr(), ws_n, _stream()))
     return y
