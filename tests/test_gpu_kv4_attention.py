@@ -151,6 +151,18 @@ def test_parts_joined_without_a_workspace(D, group, page, share, max_q, longest)
     m.check_status()
 
 
+@pytest.mark.parametrize("D,group,page", [(128, 64, 64), (64, 32, 16)])
+@pytest.mark.parametrize("hk,share,q_lens,kv_lens", [
+    (50, 1, [520, 40], [1100, 700]), (13, 4, [200, 0, 130], [1300, 0, 260]), (80, 1, [40, 33], [6400, 6161]), (80, 1, [40], [6400])])
+@pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 300)])
+def test_the_last_round_of_row_tiles_is_split(D, group, page, hk, share, q_lens, kv_lens, causal, window):
+    """More row tiles than SMs, a part of them in pieces: short and empty sequences among them, rows behind the last."""
+    m = wlq()
+    a = make(hk + D, q_lens, kv_lens, hk, share, D, group, page, tail=3)
+    check(m, *a, hk, causal, window)
+    m.check_status()
+
+
 def test_scores_that_grow_move_the_maximum():
     """Keys whose scores climb by far more than the lazy maximum's 2^8, then fall; the largest last, first and in between."""
     m = wlq()

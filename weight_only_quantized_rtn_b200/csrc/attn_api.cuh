@@ -117,11 +117,12 @@ constexpr int kPlanSms = 148;  // the SMs of a B200: plans, and with them worksp
 struct DecPlan {
     bool chunk = false, cluster = false;
     int nt = 1, row_tiles = 1, splits = 1;
+    int64_t whole = 0, tiles = 0;  // chunk: row tiles in one piece, all row tiles
     size_t off_ml = 0, ws = 0;
 };
 
-DecPlan dec_plan(int64_t tokens, int batch, int max_q, int64_t max_kv, int q_heads, int kv_heads, int head_dim, int window,
-                 int sms) {
+DecPlan dec_plan(int64_t tokens, int batch, int max_q, int64_t max_kv, int q_heads, int kv_heads, int head_dim, bool causal,
+                 int window, int sms) {
     DecPlan p;
     const int64_t rows = static_cast<int64_t>(max_q) * (q_heads / kv_heads);
     // Up to 32 rows the few-row kernel, which reads the cache once for each 16 (8 sequences of 8192, 1 of 32768, 32 of
@@ -134,8 +135,20 @@ DecPlan dec_plan(int64_t tokens, int batch, int max_q, int64_t max_kv, int q_hea
     const int64_t base = static_cast<int64_t>(batch) * kv_heads * p.row_tiles;
     const int64_t units = cdiv(seen, p.chunk ? wlq::CH_KEYS : wlq::DEC_UNIT);
     if (p.chunk) {
-        // one CTA an SM: split where the row tiles leave half of them idle, four steps a part at least
-        p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms / base, units / 4, 32})));
+        // One CTA an SM: whole rounds of row tiles stay in one piece, those of the last round are split over its SMs, with
+        // at least four steps a part (1560 queries over 7800 tokens, D = 128: 154 tiles 194 us against 282, 196 tiles 225
+        // against 302, 448 tiles 472 against 581; over 3120: 154 tiles 101 against 127).  Up to 98 of them in three
+        // parts, two rounds, where the third saved is worth the parts' traffic (76 left: 288 against 300 us for 61 steps,
+        // but 151 against 138 for 25).  Causal prompts end with their shortest tiles: those stay whole.
+        p.tiles = base;
+        p.whole = base / sms * sms;
+        const int64_t tail = base - p.whole;
+        const bool uneven = causal && static_cast<int64_t>(max_q) * 2 > max_kv;
+        if (tail > 0 && tail * 2 <= sms && (p.whole == 0 || !uneven))
+            p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms / tail, units / 4, 32})));
+        else if (tail > 0 && tail * 3 <= sms * 2 && units >= 48 && !uneven)
+            p.splits = 3;
+        if (p.splits == 1) p.whole = base;
     } else {
         // Many sequences: about three rounds of four CTAs an SM, so that ragged ones even out, with at least four
         // units for each warp of a part.  Few: one round (37 parts a head against 111 took 85 us against 100 for two
@@ -150,7 +163,8 @@ DecPlan dec_plan(int64_t tokens, int batch, int max_q, int64_t max_kv, int q_hea
         p.cluster = p.splits > 1 && p.splits <= 8 && units <= 32ll * p.splits;
     }
     if (p.splits > 1 && !p.cluster) {
-        const size_t parts = static_cast<size_t>(tokens) * q_heads * p.splits;
+        const size_t rows_kept = p.chunk ? static_cast<size_t>(p.tiles - p.whole) * (2 * wlq::CH_ROWS) : static_cast<size_t>(tokens) * q_heads;
+        const size_t parts = rows_kept * p.splits;
         p.off_ml = align256(parts * head_dim * sizeof(float));
         p.ws = p.off_ml + align256(parts * sizeof(float2));
     }
@@ -187,7 +201,8 @@ cudaError_t launch_dec(unsigned grid, cudaStream_t s, const wlq::AttnArgs& a, De
 
 template <int D>
 wlq_status launch_attention(const wlq::AttnArgs& a, const DecPlan& p, DeviceInfo* d, cudaStream_t s) {
-    const int64_t grid = static_cast<int64_t>(a.B.batch) * a.P.heads * p.row_tiles * p.splits;
+    const int64_t grid = p.chunk ? p.whole + (p.tiles - p.whole) * p.splits
+                                 : static_cast<int64_t>(a.B.batch) * a.P.heads * p.row_tiles * p.splits;
     if (grid >= (int64_t(1) << 31)) return fail(WLQ_ERR_SHAPE, "too many queries in one call");
     const unsigned gx = static_cast<unsigned>(grid);
     cudaError_t e;
@@ -206,7 +221,9 @@ wlq_status launch_attention(const wlq::AttnArgs& a, const DecPlan& p, DeviceInfo
     } else {
         e = p.nt == 1 ? launch_dec<D, 1, 1>(gx, s, a, d) : launch_dec<D, 2, 1>(gx, s, a, d);
     }
-    if (e == cudaSuccess && p.splits > 1 && !p.cluster) {
+    if (e == cudaSuccess && p.splits > 1 && p.chunk) {
+        e = launch_k(wlq::kv4_chunk_combine_kernel<D>, static_cast<unsigned>((p.tiles - p.whole) * (2 * wlq::CH_ROWS / 8)), 256, 0, s, a);
+    } else if (e == cudaSuccess && p.splits > 1 && !p.cluster) {
         const int64_t units = static_cast<int64_t>(a.B.batch) * a.B.max_q * a.q_heads;
         if (units >= (int64_t(1) << 31)) return fail(WLQ_ERR_SHAPE, "too many queries in one call");
         e = launch_k(wlq::kv4_combine_kernel<D>, static_cast<unsigned>(units), 128, 0, s, a);
@@ -331,7 +348,7 @@ size_t wlq_kv4_attention_workspace(int64_t tokens, int batch, int max_q, int64_t
     if (tokens <= 0 || batch <= 0 || max_q <= 0 || max_kv < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads ||
         (head_dim != 64 && head_dim != 128))
         return 0;
-    return dec_plan(tokens, batch, max_q, max_kv, q_heads, kv_heads, head_dim, 0, kPlanSms).ws;
+    return dec_plan(tokens, batch, max_q, max_kv, q_heads, kv_heads, head_dim, false, 0, kPlanSms).ws;
 }
 
 wlq_status wlq_kv4_attention(const void* q, int64_t q_stride, int64_t tokens, int q_heads, int kv_heads, int head_dim,
@@ -356,7 +373,7 @@ wlq_status wlq_kv4_attention(const void* q, int64_t q_stride, int64_t tokens, in
     if ((st = check_rows("q", q, q_stride, q_heads, head_dim)) != WLQ_OK) return st;
     if (!out) return fail(WLQ_ERR_INVALID_ARG, "out: null pointer");
     if (!aligned16(out) || !aligned4(lse)) return fail(WLQ_ERR_ALIGN, "out must be 16-byte aligned, lse 4-byte");
-    const DecPlan p = dec_plan(tokens, batch, max_q, max_kv, q_heads, kv_heads, head_dim, window, kPlanSms);
+    const DecPlan p = dec_plan(tokens, batch, max_q, max_kv, q_heads, kv_heads, head_dim, causal != 0, window, kPlanSms);
     if (p.ws > 0) {
         if (!workspace || ws_bytes < p.ws) return fail(WLQ_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", p.ws, workspace ? ws_bytes : size_t(0));
         if (!aligned16(workspace)) return fail(WLQ_ERR_ALIGN, "workspace must be 16-byte aligned");
@@ -375,6 +392,7 @@ wlq_status wlq_kv4_attention(const void* q, int64_t q_stride, int64_t tokens, in
     a.lse = lse;
     a.splits = p.splits;
     a.cluster = p.cluster ? 1 : 0;
+    a.whole = static_cast<int>(p.whole);
     a.row_tiles = p.row_tiles;
     a.part_o = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.off_ml);

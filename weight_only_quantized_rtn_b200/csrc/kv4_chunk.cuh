@@ -28,8 +28,9 @@
 // Bound: the exponentials (16 a clock and SM) and the tensor cores, which take
 // the same time for D = 128: 4 x 512 clocks of MMAs and 2 x 1024 of
 // exponentials for 256 rows x 128 tokens.  Measured: 1560 queries over 7800
-// tokens, 32 heads, 298 us (669 TFLOP/s; 4300 clocks a step, tensor pipe 32 %
-// active, exponentials 44 %).  One warpgroup for keys and values took 424 us,
+// tokens, 32 heads, 286 us (697 TFLOP/s; 298 before the 76 of its 224 row tiles
+// that a second round of 148 CTAs took were split; 4300 clocks a step, tensor
+// pipe 32 % active, exponentials 44 %).  One warpgroup for keys and values took 424 us,
 // weights handed over whole 352; 64-column score buffers used in turn, so that
 // no softmax waits for PV and QK, 317 to 326 against 309 then: the softmax
 // warps set the pace.
@@ -99,6 +100,61 @@ struct ChRange {
     __device__ __forceinline__ bool at(int j) const { return j >= jb && j < je; }
 };
 
+// The CTA's row tile and its part of the cached tokens: late row tiles (the longest, where causal) first, a.whole of
+// them in one piece, then the others in a.splits parts.
+struct ChTile {
+    int h, b, rt, split, parts;
+    int64_t part;  // first row of the tile's parts
+    __device__ __forceinline__ ChTile(const AttnArgs& a, int idx) : split(0), parts(1), part(0) {
+        if (idx >= a.whole) {
+            const int i = idx - a.whole;
+            parts = a.splits;
+            split = i % parts;
+            idx = a.whole + i / parts;
+            part = static_cast<int64_t>(i / parts) * (2 * CH_ROWS);
+        }
+        h = idx % a.P.heads;
+        idx /= a.P.heads;
+        b = idx % a.B.batch;
+        rt = a.row_tiles - 1 - idx / a.B.batch;
+    }
+};
+
+// Joins the parts of the split row tiles, in order: a warp for each row.
+template <int D>
+__global__ void __launch_bounds__(256) kv4_chunk_combine_kernel(const AttnArgs a) {
+    constexpr int V = D / 32;
+    grid_dependency_sync();
+    const int lane = threadIdx.x & 31, r = (blockIdx.x * 8 + (threadIdx.x >> 5)) % (2 * CH_ROWS);
+    const ChTile at(a, a.whole + static_cast<int>(blockIdx.x / (2 * CH_ROWS / 8)) * a.splits);
+    const int64_t r0 = a.B.cu[at.b], r1 = a.B.cu[at.b + 1];
+    if (kv_sequence(r0, r1, a.B.kv_len[at.b], a.B.max_q, a.B.tokens) != KV_OK) return;
+    const int row = at.rt * 2 * CH_ROWS + r;
+    if (row >= static_cast<int>(r1 - r0) * a.share) return;
+    const int64_t head_row = (r0 + row / a.share) * a.q_heads + at.h * a.share + row % a.share, first = (at.part + r) * a.splits;
+    const float2* ml = a.part_ml + first;
+    const float* po = a.part_o + first * D + lane * V;
+    float M = -INFINITY, L = 0.0f, acc[V] = {};
+    for (int s = 0; s < a.splits; ++s) M = fmaxf(M, ml[s].x);
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+        const float2 x = ml[s];
+        const float w = M == -INFINITY ? 0.0f : ex2(x.x - M);
+        L += w * x.y;
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+            const float2 o = *reinterpret_cast<const float2*>(po + static_cast<int64_t>(s) * D + k);
+            acc[k] += w * o.x;
+            acc[k + 1] += w * o.y;
+        }
+    }
+    const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
+#pragma unroll
+    for (int k = 0; k < V; k += 2)
+        *reinterpret_cast<__nv_bfloat162*>(a.out + head_row * D + lane * V + k) = __floats2bfloat162_rn(acc[k] * inv, acc[k + 1] * inv);
+    if (a.lse && lane == 0) a.lse[head_row] = L > 0.0f ? (M + __log2f(L)) * 0.6931471805599453f : (L == 0.0f ? -INFINITY : L);
+}
+
 template <int D>
 __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs a, uint64_t timeout_ns) {
     constexpr uint32_t TILE = ch_tile_bytes<D>();
@@ -125,13 +181,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dependency_sync();
-    // late row tiles (the longest, where causal) first
-    int idx = blockIdx.x;
-    const int split = idx % a.splits;
-    idx /= a.splits;
-    const int h = idx % a.P.heads;
-    idx /= a.P.heads;
-    const int b = idx % a.B.batch, rt = a.row_tiles - 1 - idx / a.B.batch;
+    const ChTile at(a, blockIdx.x);
+    const int h = at.h, b = at.b, rt = at.rt;
     const int64_t r0 = a.B.cu[b], r1 = a.B.cu[b + 1];
     const int kv = a.B.kv_len[b];
     const KvRange seq = kv_sequence(r0, r1, kv, a.B.max_q, a.B.tokens);
@@ -152,8 +203,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
         seen_range(a, kv - n + (min(rows, row0 + 2 * CH_ROWS) - 1) / a.share, kv, unused, hi);
         hi = min(hi, cover);
         const int u0 = lo / CH_KEYS, u1 = hi > 0 ? (hi - 1) / CH_KEYS + 1 : 0, units = max(0, u1 - u0);
-        j0 = u0 + static_cast<int>(static_cast<int64_t>(units) * split / a.splits);
-        j1 = u0 + static_cast<int>(static_cast<int64_t>(units) * (split + 1) / a.splits);
+        j0 = u0 + static_cast<int>(static_cast<int64_t>(units) * at.split / at.parts);
+        j1 = u0 + static_cast<int>(static_cast<int64_t>(units) * (at.split + 1) / at.parts);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const int f = row0 + t * CH_ROWS, l = min(rows, f + CH_ROWS) - 1;
@@ -326,6 +377,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
         if (ok) {
             tc_fence_after();
             const int64_t head_row = token * a.q_heads + head;
+            const int64_t part = (at.part + row - row0) * at.parts + at.split;
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
 #pragma unroll
             for (int d = 0; d < D; d += 16) {
@@ -337,7 +389,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = 0;
                 }
-                if (live && a.splits == 1) {
+                if (live && at.parts == 1) {
                     uint32_t o[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -348,14 +400,14 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
                     dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
                     dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
                 } else if (live) {
-                    uint4* dst = reinterpret_cast<uint4*>(a.part_o + (head_row * a.splits + split) * D + d);
+                    uint4* dst = reinterpret_cast<uint4*>(a.part_o + part * D + d);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 }
                 __syncwarp();
             }
             if (live) {
-                if (a.splits > 1) a.part_ml[head_row * a.splits + split] = make_float2(m, l);
+                if (at.parts > 1) a.part_ml[part] = make_float2(m, l);
                 else if (a.lse) a.lse[head_row] = l > 0.0f ? (m + __log2f(l)) * 0.6931471805599453f : (l == 0.0f ? -INFINITY : l);
             }
             tc_fence_before();

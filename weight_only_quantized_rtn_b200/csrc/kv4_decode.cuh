@@ -61,9 +61,10 @@ struct AttnArgs {
     int causal, window;
     uint16_t* out;
     float* lse;
-    float* part_o;   // [tokens * q_heads][splits][D]
-    float2* part_ml;  // [tokens * q_heads][splits]: (m, l)
+    float* part_o;   // [tokens * q_heads][splits][D]; many rows: [rows of the split tiles][splits][D]
+    float2* part_ml;  // the same without D: (m, l)
     int splits, row_tiles;
+    int whole;    // many rows: the row tiles that are not split
     int cluster;  // the splits are the CTAs of a cluster, which joins their parts itself
 };
 
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
     const int mat = lane >> 3, mr = lane & 7;
     int stage = 0;
     for (int u = ub + warp; u < ue; u += DEC_WARPS) {
-        // the unit two ahead, into the stage read last
+        // the unit DEC_STAGES - 1 ahead, into the stage read last
         {
             const int ahead = u + (DEC_STAGES - 1) * DEC_WARPS, st = stage == 0 ? DEC_STAGES - 1 : stage - 1;
             if (ahead < ue) fetch(ahead, pg[DEC_STAGES - 1], ring + st * R::STAGE);
