@@ -30,7 +30,7 @@
 // exponentials for 256 rows x 128 tokens.  Measured: 1560 queries over 7800
 // tokens, 32 heads, 286 us (697 TFLOP/s; 298 before the 76 of its 224 row tiles
 // that a second round of 148 CTAs took were split; 4300 clocks a step, tensor
-// pipe 32 % active, exponentials 44 %).  One warpgroup for keys and values took 424 us,
+// pipe 34 % active, exponentials 40 %).  One warpgroup for keys and values took 424 us,
 // weights handed over whole 352; 64-column score buffers used in turn, so that
 // no softmax waits for PV and QK, 317 to 326 against 309 then: the softmax
 // warps set the pace.
