@@ -234,8 +234,9 @@ __global__ void __launch_bounds__(I8_THREADS, 1)
                 if constexpr (PAIR) mma_commit_pair_both_on(on, &accfull[buf]);
                 else mma_commit_on(on, &accfull[buf]);
             }
-            // every MMA issued has completed before tensor memory is freed (a pair's second CTA only sees its copy arrive)
-            if constexpr (PAIR) mma_commit_pair_both_on(on, drain);
+            // every MMA issued has completed before tensor memory is freed.  Signalled in this CTA only: the
+            // pair's second CTA does not wait for it, and an arrival may not reach a CTA that has left.
+            if constexpr (PAIR) mma_commit_pair_on(on, drain);
             else mma_commit_on(on, drain);
             const uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < a.timeout_ns) {

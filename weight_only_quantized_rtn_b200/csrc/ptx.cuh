@@ -189,6 +189,14 @@ __device__ __forceinline__ void mma_commit_on(uint32_t on, uint64_t* bar) {
         "r"(on)
         : "memory");
 }
+__device__ __forceinline__ void mma_commit_pair_on(uint32_t on, uint64_t* bar) {  // a pair's MMAs, signalled in this CTA only
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(on)
+        : "memory");
+}
 __device__ __forceinline__ void mma_commit_pair_both_on(uint32_t on, uint64_t* bar) {  // pair of cluster ranks 0 and 1
     asm volatile(
         "{\n\t.reg .pred q;\n\t"
