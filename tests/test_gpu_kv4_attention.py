@@ -349,3 +349,26 @@ def test_workspaces_that_are_views_of_less_memory_are_refused():
     x, wq, s = torch.zeros(4, 128, device="cuda").bfloat16(), torch.zeros(16, 128, dtype=torch.int8, device="cuda"), torch.ones(16, device="cuda")
     with pytest.raises(m.WlqError, match="contiguous"):
         m.w8a8_linear(x, wq, s, workspace=torch.empty(1, dtype=torch.uint8, device="cuda").expand(m.w8a8_workspace(4, 128)))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("size", [1e-33, 1e-36, 2e-39, 9.2e-41])
+def test_queries_next_to_zero(D, n, size):
+    """Rows whose largest value is next to bf16's smallest, with zeros in them (9.2e-41 is the smallest subnormal): nearly
+    the mean of the values, at a scale that hardly matters and at one that lifts the scores."""
+    m = wlq()
+    q, *a = make(D + n, [n, 1], [n + 300, 70], 2, 2, D, 32, 16)
+    q = q.clone()
+    small = (torch.rand(q.shape, generator=torch.Generator().manual_seed(1)) * size).cuda().bfloat16()
+    q[0] = small[0]
+    q[-1, 1:] = small[-1, 1:]
+    q[0, :, ::3] = 0
+    q[-1, 1, 1:] = 0
+    q[-1, 1, 0] = size
+    assert torch.isfinite(q).all() and float(q[0].float().abs().max()) > 0
+    check(m, q, *a, 2, True, 0, random=False)
+    m.check_status()
+    q[:] = small
+    check(m, q, *a, 2, True, 0, scale=0.01 / size if size > 1e-38 else 1e38, random=False)
+    m.check_status()

@@ -110,14 +110,13 @@ __device__ __forceinline__ void seen_range(const AttnArgs& a, int p, int kv, int
 
 // 2^e that puts the largest |q| of a row into [2^14, 2^15) (1 for zero or
 // non-finite rows): every bf16 value down to 2^-31 of it is then exact in fp16.
+// At most 2^126, which stays an fp32 number and takes bf16's smallest value,
+// 2^-133, to 2^-7.
 __device__ __forceinline__ int row_exponent(uint32_t absmax_bits16) {
     const int ex = static_cast<int>(absmax_bits16 >> 7);  // biased exponent
-    return (absmax_bits16 == 0 || ex == 255) ? 0 : 14 + 127 - max(ex, 1);
+    return (absmax_bits16 == 0 || ex == 255) ? 0 : min(14 + 127 - ex, 126);
 }
-__device__ __forceinline__ float pow2f(int e) {  // 2^e for e in [-252, 252]: two exact factors
-    const int h = e / 2;
-    return __uint_as_float(static_cast<uint32_t>(127 + h) << 23) * __uint_as_float(static_cast<uint32_t>(127 + e - h) << 23);
-}
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }  // -126 <= e <= 127
 
 // 16 bytes from global to shared memory, asynchronously.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
