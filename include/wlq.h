@@ -470,7 +470,9 @@ wlq_status wlq_kv4_read(const int32_t* cu_seqlens, const int32_t* kv_lens, int b
  * power of two per row (exact unless a value lies 2^-29 below its row's
  * largest); at most 32 rows (queries x q_heads / kv_heads) of a sequence: keys
  * and values as their codes (exact), weights as exp(. - max) times the value's
- * scale; more rows: keys and values as code * scale, weights as exp(. - max).
+ * scale (off by 2^-11 of it, or 2^-25 of the largest such product that the row
+ * and group have seen); more rows: keys and values as code * scale, weights as
+ * exp(. - max) (off by 2^-11, or 2^-25 of the largest weight).
  * Results are bitwise reproducible run to run.
  * workspace: wlq_kv4_attention_workspace() bytes (0: none needed), 16-byte
  * aligned, contents need no initialisation; calls that may overlap on the GPU

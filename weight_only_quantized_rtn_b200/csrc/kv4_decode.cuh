@@ -12,9 +12,17 @@
 //    so the scores of each group are accumulated apart and scaled in fp32;
 //  - V: an MMA's 16 outputs lie in one such block too, so the scale goes into
 //    the weights: P' = 2^(x - M) vs, one fp16 rounding (2^-11).  The reference
-//    M is the running maximum of the scores plus the exponent E of the largest
-//    V scale so far, so P' stays below 2^9 whatever the scales are; l is summed
-//    with the same M and cancels it.
+//    M is the running maximum m of the scores plus E - 6, E the exponent of the
+//    largest V scale so far, so P' stays below 2^15; l is summed with the same
+//    M and cancels it.  That holds while a warp meets only scales within 2^7 of
+//    each other: a product that is an fp16 subnormal is then off by at most
+//    2^-25 of the largest product of its row and group.
+//  - From the first scale further off on, the warp's rows and groups have
+//    factors of their own: P' = 2^(x - m) vs f, where f keeps the largest product
+//    of THIS row and group between 2^6 and 2^15.  Otherwise one token or group
+//    with large values, seen or not, would cost all others their bits.  The
+//    factors lie in shared memory; with them alone (no common reference) 64
+//    ragged sequences took 120 us against 107, two long ones 88 against 73.
 // ldmatrix hands a lane word t of 16 bytes of row g (K), and with .trans the
 // 16-bit pieces of two tokens side by side (V): four inputs of a token pair,
 // one mask-or and one exact fp16 operation from the MMA's operand.  P^T moves
@@ -40,6 +48,7 @@
 // it is and was no faster.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include "kvcache.cuh"
@@ -50,6 +59,9 @@ namespace wlq {
 constexpr int DEC_WARPS = 4;
 constexpr int DEC_UNIT = 32;           // tokens of one warp step
 constexpr float ATT_LAZY = 8.0f;       // how far a score may pass the running maximum (log2)
+constexpr int DEC_ROOM = 6;            // P' = weight * V scale * 2^6 against the references: at most 2^(8 + 1 + 6), an fp16 number
+constexpr float DEC_TOP = 32768.0f;    // how large P' may get with factors of its own
+constexpr float DEC_FMAX = 7.922816251426434e28f;  // 2^96, the largest factor: times a weight (2^8) and a scale (2^13.2) still an fp32 number
 
 struct AttnArgs {
     const uint16_t* q;
@@ -163,10 +175,13 @@ struct DecRing {
 };
 template <int D, int NT>
 __host__ __device__ constexpr size_t dec_out_bytes() { return static_cast<size_t>(DEC_WARPS) * 8 * NT * (D + 4) * 4 + DEC_WARPS * 8 * NT * 8; }
+// The rings, after them the parts; behind both the warps' factors, [nt][group][8 rows].
 template <int D, int NT, int G>
-__host__ __device__ constexpr size_t dec_smem_bytes() {
+__host__ __device__ constexpr size_t dec_factors_at() {
     return DecRing<D, G>::BYTES > dec_out_bytes<D, NT>() ? DecRing<D, G>::BYTES : dec_out_bytes<D, NT>();
 }
+template <int D, int NT, int G>
+__host__ __device__ constexpr size_t dec_smem_bytes() { return dec_factors_at<D, NT, G>() + DEC_WARPS * NT * G * 8 * sizeof(float); }
 
 // Pages of a unit's two 16-token tiles (0xFFFFFFFF: no token of the range, or out of range).
 __device__ __forceinline__ void dec_pages(const AttnArgs& a, const int32_t* table, int unit, int ue, int end, uint32_t (&pg)[2]) {
@@ -224,11 +239,11 @@ struct DecFetch {
     }
 };
 
-// G fp16 scales of one token, two a word (G == 1: one, the other half 0).
+// G fp16 scales of one token, two a word (G == 1: one in both halves).
 template <int G>
 __device__ __forceinline__ void load_scales(const uint8_t* p, uint32_t (&s)[(G + 1) / 2]) {
     if constexpr (G == 1) {
-        s[0] = *reinterpret_cast<const uint16_t*>(p);
+        s[0] = *reinterpret_cast<const uint16_t*>(p) * 0x10001u;
     } else if constexpr (G == 2) {
         s[0] = *reinterpret_cast<const uint32_t*>(p);
     } else {
@@ -329,9 +344,13 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
             seen_range(a, kv - n + cr / a.share, kv, clo[nt][k], chi[nt][k]);
         }
     }
-    // m: running maximum of the scores, ev: exponent of the largest V scale so far; M = m + ev
-    float m[NT][2], l[NT][2], o[NT][2 * W][4], ev = -24.0f;
-    uint32_t vtop = 0;  // fp16 bits of 2^ev's upper end: a larger scale moves ev
+    // m: running maximum of the scores; ev: E - 6, E the exponent of the largest V scale so far; M = m + ev
+    float m[NT][2], l[NT][2], o[NT][2 * W][4], ev = -24.0f - DEC_ROOM;
+    __half2 vtop = bits_h2(0u);             // (twice) 2^E's upper end: a larger scale moves E
+    __half2 vlow = bits_h2(0u);             // 2^(E - 6): a smaller scale asks for factors
+    __half2 vleast = bits_h2(0x7C007C00u);  // the smallest scales this lane has met
+    float* factors = reinterpret_cast<float*>(dec_smem + dec_factors_at<D, NT, G>()) + warp * NT * G * 8 + 2 * t;  // of this lane's rows
+    auto factor = [&](int nt, int i) -> float2& { return *reinterpret_cast<float2*>(factors + (nt * G + i) * 8); };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -348,185 +367,315 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
     // ldmatrix rows of this lane.  K, D = 128: matrices are the blocks 0..3 of 8 rows; D = 64: blocks 0, 1 of
     // rows 0..7, then of rows 8..15.  V: blocks (2 i, tokens 0..7), (2 i, 8..15), (2 i + 1, ...), ...
     const int mat = lane >> 3, mr = lane & 7;
-    int stage = 0;
-    for (int u = ub + warp; u < ue; u += DEC_WARPS) {
-        // the unit DEC_STAGES - 1 ahead, into the stage read last
-        {
-            const int ahead = u + (DEC_STAGES - 1) * DEC_WARPS, st = stage == 0 ? DEC_STAGES - 1 : stage - 1;
-            if (ahead < ue) fetch(ahead, pg[DEC_STAGES - 1], ring + st * R::STAGE);
-            cp_async_commit();
-        }
-        cp_async_wait<DEC_STAGES - 1>();
-        __syncwarp();
-        const uint32_t sk = ring + stage * R::STAGE, sv = sk + R::CODES;
-        const uint8_t* sc = dec_smem + (sk - smem_u32(dec_smem)) + 2 * R::CODES;
-        const int tok0 = u * DEC_UNIT;
-        const bool in0 = pg[0][0] < fetch.npages, in1 = pg[0][1] < fetch.npages;
-        const bool inside = tok0 >= lo_all && tok0 + DEC_UNIT <= hi_all && in0 && in1;
-        if (!inside && ((!in0 && tok0 < hi) || (!in1 && tok0 + 16 < hi)) && lane == 0) raise_error(ERRBIT_INDEX);
-        float x[2][NT][4];
-        uint32_t vs[2][2][(G + 1) / 2];
+    int stage = 0, u = ub + warp;
+    bool apart = false;  // the rows and groups have factors of their own
+    auto walk = [&](auto apart_tag) {  // the units, until one asks for factors
+        constexpr bool APART = decltype(apart_tag)::value;
+        bool fetched = APART;  // that unit's copies are there and the next one's on their way
+        for (; u < ue; u += DEC_WARPS) {
+            // the unit DEC_STAGES - 1 ahead, into the stage read last
+            if (!fetched) {
+                const int ahead = u + (DEC_STAGES - 1) * DEC_WARPS, st = stage == 0 ? DEC_STAGES - 1 : stage - 1;
+                if (ahead < ue) fetch(ahead, pg[DEC_STAGES - 1], ring + st * R::STAGE);
+                cp_async_commit();
+            }
+            fetched = false;
+            cp_async_wait<DEC_STAGES - 1>();
+            __syncwarp();
+            const uint32_t sk = ring + stage * R::STAGE, sv = sk + R::CODES;
+            const uint8_t* sc = dec_smem + (sk - smem_u32(dec_smem)) + 2 * R::CODES;
+            const int tok0 = u * DEC_UNIT;
+            const bool in0 = pg[0][0] < fetch.npages, in1 = pg[0][1] < fetch.npages;
+            const bool inside = tok0 >= lo_all && tok0 + DEC_UNIT <= hi_all && in0 && in1;
+            if (!inside && ((!in0 && tok0 < hi) || (!in1 && tok0 + 16 < hi)) && lane == 0) raise_error(ERRBIT_INDEX);
+            float x[2][NT][4];
+            uint32_t vs[2][2][(G + 1) / 2];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-            float acc[NT][G][4];
+            for (int mt = 0; mt < 2; ++mt) {
+                float acc[NT][G][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < G; ++i)
+                    for (int i = 0; i < G; ++i)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[nt][i][k] = 0.0f;
-            uint32_t kr[2][W];  // words t of the row's blocks, rows g and g + 8
-            if constexpr (D == 128) {
-                uint32_t q0[4], q1[4];
-                ldsm_x4(sk + R::at(16 * mt + mr, mat), q0);
-                ldsm_x4(sk + R::at(16 * mt + 8 + mr, mat), q1);
+                        for (int k = 0; k < 4; ++k) acc[nt][i][k] = 0.0f;
+                uint32_t kr[2][W];  // words t of the row's blocks, rows g and g + 8
+                if constexpr (D == 128) {
+                    uint32_t q0[4], q1[4];
+                    ldsm_x4(sk + R::at(16 * mt + mr, mat), q0);
+                    ldsm_x4(sk + R::at(16 * mt + 8 + mr, mat), q1);
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        kr[0][w] = q0[w];
+                        kr[1][w] = q1[w];
+                    }
+                } else {
+                    uint32_t q[4];
+                    ldsm_x4(sk + R::at(16 * mt + 8 * (mat >> 1) + mr, mat & 1), q);
+                    kr[0][0] = q[0]; kr[0][1] = q[1]; kr[1][0] = q[2]; kr[1][1] = q[3];
+                }
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
-                    kr[0][w] = q0[w];
-                    kr[1][w] = q1[w];
+                    uint32_t fa[4], fb[4];
+                    nibbles_codes(kr[0][w], fa);
+                    nibbles_codes(kr[1][w], fb);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma16816_f16(acc[nt][w / BPG], fa[0], fb[0], fa[1], fb[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
+                        mma16816_f16(acc[nt][w / BPG], fa[2], fb[2], fa[3], fb[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+                    }
                 }
-            } else {
-                uint32_t q[4];
-                ldsm_x4(sk + R::at(16 * mt + 8 * (mat >> 1) + mr, mat & 1), q);
-                kr[0][0] = q[0]; kr[0][1] = q[1]; kr[1][0] = q[2]; kr[1][1] = q[3];
-            }
+                uint32_t ks[2][(G + 1) / 2];
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                uint32_t fa[4], fb[4];
-                nibbles_codes(kr[0][w], fa);
-                nibbles_codes(kr[1][w], fb);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma16816_f16(acc[nt][w / BPG], fa[0], fb[0], fa[1], fb[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
-                    mma16816_f16(acc[nt][w / BPG], fa[2], fb[2], fa[3], fb[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+                for (int r = 0; r < 2; ++r) {
+                    load_scales<G>(sc + (16 * mt + 8 * r + g) * G * 2, ks[r]);
+                    load_scales<G>(sc + R::SCALES + (16 * mt + 8 * r + g) * G * 2, vs[mt][r]);
                 }
-            }
-            uint32_t ks[2][(G + 1) / 2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                load_scales<G>(sc + (16 * mt + 8 * r + g) * G * 2, ks[r]);
-                load_scales<G>(sc + R::SCALES + (16 * mt + 8 * r + g) * G * 2, vs[mt][r]);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float s = acc[nt][0][k] * scale_of(ks[k >> 1], 0);
-#pragma unroll
-                    for (int i = 1; i < G; ++i) s = fmaf(acc[nt][i][k], scale_of(ks[k >> 1], i), s);
-                    x[mt][nt][k] = s * cs[nt][k & 1];
-                }
-        }
-        if (!inside) {
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int tok = tok0 + 16 * mt + 8 * (k >> 1) + g;
-                        if (tok < clo[nt][k & 1] || tok >= chi[nt][k & 1] || !(mt ? in1 : in0)) x[mt][nt][k] = -INFINITY;
+                        float s = acc[nt][0][k] * scale_of(ks[k >> 1], 0);
+#pragma unroll
+                        for (int i = 1; i < G; ++i) s = fmaf(acc[nt][i][k], scale_of(ks[k >> 1], i), s);
+                        x[mt][nt][k] = s * cs[nt][k & 1];
                     }
-            // places no token was written to may hold anything
+            }
+            __half2 least = bits_h2(0x7C007C00u);  // the unit's smallest scales
+            if (!inside) {
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+                for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    if (tok0 + 16 * mt + 8 * r + g >= kv || !(mt ? in1 : in0))
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int i = 0; i < (G + 1) / 2; ++i) vs[mt][r][i] = 0;
-        }
-        __half2 vm2 = bits_h2(0u);
+                        for (int k = 0; k < 4; ++k) {
+                            const int tok = tok0 + 16 * mt + 8 * (k >> 1) + g;
+                            if (tok < clo[nt][k & 1] || tok >= chi[nt][k & 1] || !(mt ? in1 : in0)) x[mt][nt][k] = -INFINITY;
+                        }
+                // places no token was written to may hold anything
 #pragma unroll
-        for (int i = 0; i < (G + 1) / 2; ++i)
-            vm2 = __hmax2(vm2, __hmax2(__hmax2(bits_h2(vs[0][0][i]), bits_h2(vs[0][1][i])), __hmax2(bits_h2(vs[1][0][i]), bits_h2(vs[1][1][i]))));
-        uint32_t vmax = max(h2_bits(vm2) & 0xFFFFu, h2_bits(vm2) >> 16);
-        bool move = vmax > vtop;
+                for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+                    for (int r = 0; r < 2; ++r) {
+                        const bool none = tok0 + 16 * mt + 8 * r + g >= kv || !(mt ? in1 : in0);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                move |= fmaxf(fmaxf(x[0][nt][k], x[0][nt][2 + k]), fmaxf(x[1][nt][k], x[1][nt][2 + k])) > m[nt][k] + ATT_LAZY;
-        if (__any_sync(0xffffffffu, move)) {
-            // a new reference: the largest scores, the exponent of the largest V scale
-            vmax = __reduce_max_sync(0xffffffffu, vmax);
-            float step = 0.0f;
-            if (vmax > vtop) {
-                vtop = vmax | 0x03FFu;  // up to the next power of two (subnormals: 2^-14)
-                const float en = static_cast<float>(max(static_cast<int>(vtop >> 10), 1) - 15);
-                step = en - ev;
-                ev = en;
+                        for (int i = 0; i < (G + 1) / 2; ++i) {
+                            if (none) vs[mt][r][i] = 0;
+                            else least = __hmin2(least, bits_h2(vs[mt][r][i]));
+                        }
+                    }
+            }
+            bool move = false;
+            __half2 vm2 = bits_h2(0u);
+            if constexpr (!APART) {
+#pragma unroll
+                for (int i = 0; i < (G + 1) / 2; ++i)
+                    vm2 = __hmax2(vm2, __hmax2(__hmax2(bits_h2(vs[0][0][i]), bits_h2(vs[0][1][i])), __hmax2(bits_h2(vs[1][0][i]), bits_h2(vs[1][1][i]))));
+                __half2 vn2 = bits_h2(0x7C007C00u);
+#pragma unroll
+                for (int i = 0; i < (G + 1) / 2; ++i)
+                    vn2 = __hmin2(vn2, __hmin2(__hmin2(bits_h2(vs[0][0][i]), bits_h2(vs[0][1][i])), __hmin2(bits_h2(vs[1][0][i]), bits_h2(vs[1][1][i]))));
+                vleast = __hmin2(vleast, inside ? vn2 : least);
+                move = !__hble2(vm2, vtop) || !__hbge2(vleast, vlow);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float top = fmaxf(fmaxf(x[0][nt][k], x[0][nt][2 + k]), fmaxf(x[1][nt][k], x[1][nt][2 + k]));
+                for (int k = 0; k < 2; ++k)
+                    move |= fmaxf(fmaxf(x[0][nt][k], x[0][nt][2 + k]), fmaxf(x[1][nt][k], x[1][nt][2 + k])) > m[nt][k] + ATT_LAZY;
+            if (__any_sync(0xffffffffu, move)) {
+                // a new reference: the largest scores, the exponent of the largest V scale
+                float step = 0.0f;
+                if constexpr (!APART) {
+                    const uint32_t vmax = __reduce_max_sync(0xffffffffu, max(h2_bits(vm2) & 0xFFFFu, h2_bits(vm2) >> 16));
+                    int e = static_cast<int>(ev);
+                    if (vmax > (h2_bits(vtop) & 0xFFFFu)) {
+                        const uint32_t top = vmax | 0x03FFu;  // up to the next power of two (subnormals: 2^-14)
+                        e = max(static_cast<int>(top >> 10), 1) - 15 - DEC_ROOM;
+                        vtop = bits_h2(top * 0x10001u);
+                        vlow = __float2half2_rn(pow2f(e));
+                    }
+                    if (__any_sync(0xffffffffu, !__hbge2(vleast, vlow))) {
+                        apart = true;
+                        return;
+                    }
+                    step = static_cast<float>(e) - ev;
+                    ev = static_cast<float>(e);
+                }
 #pragma unroll
-                    for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                    const float mn = fmaxf(m[nt][k], top);
-                    const float f = mn == -INFINITY ? 1.0f : ex2(m[nt][k] - mn - step);
-                    m[nt][k] = mn;
-                    l[nt][k] *= f;
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int d = 0; d < 2 * W; ++d) {
-                        o[nt][d][k] *= f;
-                        o[nt][d][2 + k] *= f;
+                    for (int k = 0; k < 2; ++k) {
+                        float top = fmaxf(fmaxf(x[0][nt][k], x[0][nt][2 + k]), fmaxf(x[1][nt][k], x[1][nt][2 + k]));
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                        const float mn = fmaxf(m[nt][k], top);
+                        const float fall = mn == -INFINITY ? 1.0f : ex2(m[nt][k] - mn - step);
+                        m[nt][k] = mn;
+                        l[nt][k] *= fall;
+                        if constexpr (!APART) {
+#pragma unroll
+                            for (int d = 0; d < 2 * W; ++d) {
+                                o[nt][d][k] *= fall;
+                                o[nt][d][2 + k] *= fall;
+                            }
+                        } else {  // what o holds stays, its factors grow as the weights fall
+#pragma unroll
+                            for (int i = 0; i < G; ++i) {
+                                float& f = k ? factor(nt, i).y : factor(nt, i).x;
+                                const float was = f, grown = was / fall;  // from -inf: infinite, and o is 0
+                                const float keep = grown <= DEC_FMAX ? 1.0f : DEC_FMAX * (fall / was);
+#pragma unroll
+                                for (int d = 2 * BPG * i; d < 2 * BPG * (i + 1); ++d) {
+                                    o[nt][d][k] *= keep;
+                                    o[nt][d][2 + k] *= keep;
+                                }
+                                __syncwarp();  // the row's eight lanes have read it; all write the same
+                                f = fminf(grown, DEC_FMAX);
+                            }
+                        }
+                    }
+                __syncwarp();
+            }
+            // weights, then by groups: P' = weight * V scale as the operand of both token halves
+            uint32_t pf[2][NT][G][2];
+            if constexpr (!APART) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float M[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) M[k] = m[nt][k] == -INFINITY ? 0.0f : m[nt][k] + ev;  // nothing seen yet: x is -inf too
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float p0 = ex2(x[mt][nt][2 * r] - M[0]), p1 = ex2(x[mt][nt][2 * r + 1] - M[1]);
+                            l[nt][0] += p0;
+                            l[nt][1] += p1;
+#pragma unroll
+                            for (int i = 0; i < G; ++i) {
+                                const float v = scale_of(vs[mt][r], i);
+                                pf[mt][nt][i][r] = movmatrix(h2_bits(__floats2half2_rn(p0 * v, p1 * v)));
+                            }
+                        }
+                }
+            } else {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {  // the scores become weights
+                            const float mk = m[nt][k & 1];
+                            x[mt][nt][k] = ex2(x[mt][nt][k] - (mk == -INFINITY ? 0.0f : mk));
+                            l[nt][k & 1] += x[mt][nt][k];
+                        }
+#pragma unroll
+                    for (int i = 0; i < G; ++i) {
+                        float2 f = factor(nt, i), top = make_float2(0.0f, 0.0f);
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const float v = scale_of(vs[mt][r], i);
+                                top.x = fmaxf(top.x, x[mt][nt][2 * r] * v * f.x);
+                                top.y = fmaxf(top.y, x[mt][nt][2 * r + 1] * v * f.y);
+                            }
+                        if (__any_sync(0xffffffffu, fmaxf(top.x, top.y) > DEC_TOP)) {
+                            // smaller factors where a product is too large: the largest one to 2^6
+#pragma unroll
+                            for (int off = 4; off < 32; off <<= 1)
+                                top = make_float2(fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, off)), fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, off)));
+                            const uint32_t six = (254u + DEC_ROOM) << 23;  // less top's biased exponent: 2^(6 - exponent)
+                            const float s0 = top.x > DEC_TOP ? __uint_as_float(six - (__float_as_uint(top.x) & 0x7F800000u)) : 1.0f;
+                            const float s1 = top.y > DEC_TOP ? __uint_as_float(six - (__float_as_uint(top.y) & 0x7F800000u)) : 1.0f;
+                            f = make_float2(f.x * s0, f.y * s1);
+#pragma unroll
+                            for (int d = 2 * BPG * i; d < 2 * BPG * (i + 1); ++d) {
+                                o[nt][d][0] *= s0;
+                                o[nt][d][1] *= s1;
+                                o[nt][d][2] *= s0;
+                                o[nt][d][3] *= s1;
+                            }
+                            __syncwarp();
+                            factor(nt, i) = f;
+                        }
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const float v = scale_of(vs[mt][r], i);
+                                pf[mt][nt][i][r] = movmatrix(h2_bits(__floats2half2_rn(x[mt][nt][2 * r] * v * f.x, x[mt][nt][2 * r + 1] * v * f.y)));
+                            }
                     }
                 }
-        }
-        // weights, then by groups: P' = weight * V scale as the operand of both token halves
-        uint32_t pf[2][NT][G][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float M[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) M[k] = m[nt][k] == -INFINITY ? 0.0f : m[nt][k] + ev;  // nothing seen yet: x is -inf too
+                __syncwarp();
+            }
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float p0 = ex2(x[mt][nt][2 * r] - M[0]), p1 = ex2(x[mt][nt][2 * r + 1] - M[1]);
-                    l[nt][0] += p0;
-                    l[nt][1] += p1;
+                for (int w2 = 0; w2 < W / 2; ++w2) {
+                    uint32_t vr[4];  // block 2 w2: tokens 0..7, 8..15; block 2 w2 + 1
+                    ldsm_x4_trans(sv + R::at(16 * mt + 8 * (mat & 1) + mr, 2 * w2 + (mat >> 1)), vr);
 #pragma unroll
-                    for (int i = 0; i < G; ++i) {
-                        const float v = scale_of(vs[mt][r], i);
-                        pf[mt][nt][i][r] = movmatrix(h2_bits(__floats2half2_rn(p0 * v, p1 * v)));
+                    for (int j = 0; j < 2; ++j) {
+                        const int w = 2 * w2 + j;
+                        uint32_t fa[4], fb[4];
+                        nibbles_codes(vr[2 * j], fa);
+                        nibbles_codes(vr[2 * j + 1], fb);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816_f16(o[nt][2 * w], fa[0], fa[1], fb[0], fb[1], pf[mt][nt][w / BPG][0], pf[mt][nt][w / BPG][1]);
+                            mma16816_f16(o[nt][2 * w + 1], fa[2], fa[3], fb[2], fb[3], pf[mt][nt][w / BPG][0], pf[mt][nt][w / BPG][1]);
+                        }
                     }
                 }
-        }
+            __syncwarp();  // the stage may be written again
+            stage = stage == DEC_STAGES - 1 ? 0 : stage + 1;
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int w2 = 0; w2 < W / 2; ++w2) {
-                uint32_t vr[4];  // block 2 w2: tokens 0..7, 8..15; block 2 w2 + 1
-                ldsm_x4_trans(sv + R::at(16 * mt + 8 * (mat & 1) + mr, 2 * w2 + (mat >> 1)), vr);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int w = 2 * w2 + j;
-                    uint32_t fa[4], fb[4];
-                    nibbles_codes(vr[2 * j], fa);
-                    nibbles_codes(vr[2 * j + 1], fb);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma16816_f16(o[nt][2 * w], fa[0], fa[1], fb[0], fb[1], pf[mt][nt][w / BPG][0], pf[mt][nt][w / BPG][1]);
-                        mma16816_f16(o[nt][2 * w + 1], fa[2], fa[3], fb[2], fb[3], pf[mt][nt][w / BPG][0], pf[mt][nt][w / BPG][1]);
-                    }
-                }
+            for (int i = 0; i + 1 < DEC_STAGES; ++i) {
+                pg[i][0] = pg[i + 1][0];
+                pg[i][1] = pg[i + 1][1];
             }
-        __syncwarp();  // the stage may be written again
-        stage = stage == DEC_STAGES - 1 ? 0 : stage + 1;
-#pragma unroll
-        for (int i = 0; i + 1 < DEC_STAGES; ++i) {
-            pg[i][0] = pg[i + 1][0];
-            pg[i][1] = pg[i + 1][1];
+            dec_pages(a, table, u + DEC_STAGES * DEC_WARPS, ue, hi, pg[DEC_STAGES - 1]);
         }
-        dec_pages(a, table, u + DEC_STAGES * DEC_WARPS, ue, hi, pg[DEC_STAGES - 1]);
+    };
+    walk(std::false_type{});
+    if (apart) {
+        // from the common reference to factors, which start 2^64 above it (o stays below 2^15 2^31 2^64) and come down to
+        // what each row and group needs; then the rest, from that unit on
+        const float up = pow2f(64), f = pow2f(64 - static_cast<int>(ev)), inv = pow2f(static_cast<int>(ev));
+        ev = 0.0f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            l[nt][0] *= inv;
+            l[nt][1] *= inv;
+#pragma unroll
+            for (int i = 0; i < G; ++i) factor(nt, i) = make_float2(f, f);
+#pragma unroll
+            for (int d = 0; d < 2 * W; ++d)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[nt][d][k] *= up;
+        }
+        __syncwarp();
+        walk(std::true_type{});
     }
 
     // the warps' parts, then the CTA's (over the rings)
     cp_async_wait<0>();
+    if (apart) {  // the factors off again
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                const float2 f = factor(nt, i);
+                const float inv[2] = {1.0f / f.x, 1.0f / f.y};
+#pragma unroll
+                for (int d = 2 * BPG * i; d < 2 * BPG * (i + 1); ++d)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[nt][d][k] *= inv[k & 1];
+            }
+    }
     __syncthreads();
     float* sm_o = reinterpret_cast<float*>(dec_smem);                                       // [warps][8 NT][D + 4]
     float2* sm_ml = reinterpret_cast<float2*>(dec_smem + static_cast<size_t>(DEC_WARPS) * 8 * NT * (D + 4) * 4);  // [warps][8 NT]
