@@ -457,7 +457,9 @@ wlq_status wlq_kv4_read(const int32_t* cu_seqlens, const int32_t* kv_lens, int b
  *   out = softmax_j(scale q . k_j) v_j    over the cached tokens j it sees:
  * all of them (causal 0), j <= p (causal 1), p - window < j <= p (causal 1,
  * window > 0).  Query head h reads cache head h / (q_heads / kv_heads).
- * A query that sees nothing gets zeros (lse -inf).
+ * A query that sees nothing gets zeros (lse -inf).  Pages behind the window, all
+ * of whose tokens come before the first that any of the queries sees, may have
+ * been given back: they are not read, whatever their table entries hold.
  * q   : bf16, token strides as above; out: bf16 [tokens, q_heads, head_dim],
  *       not overlapping q.  Cached scales are those the append writes (at most
  *       9328: seven of them stay finite in fp16).

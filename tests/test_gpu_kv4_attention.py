@@ -372,3 +372,38 @@ def test_queries_next_to_zero(D, n, size):
     q[:] = small
     check(m, q, *a, 2, True, 0, scale=0.01 / size if size > 1e-38 else 1e38, random=False)
     m.check_status()
+
+
+@pytest.mark.parametrize("D,group,page", [(128, 32, 16), (128, 128, 64), (64, 64, 32), (64, 32, 128)])
+@pytest.mark.parametrize("n,share", [(1, 4), (3, 8), (50, 1), (70, 4)])
+@pytest.mark.parametrize("back", ["none", "past", "other"])
+def test_pages_given_back_behind_the_window(D, group, page, n, share, back):
+    """Table entries of pages that no query sees: none (-1), past the pool, or a page that now holds something else, whose
+    scales are not finite.  They are not read: the result is that of the whole cache, without an error."""
+    m = wlq()
+    m.check_status()
+    for kv in (n + 90, n + 700, n + 701, n + 1663):
+        for window in (1, 33, 80, 600):
+            q, cache, cu, kvs, table = make(kv + share, [n, 1], [kv, 5], 2, share, D, group, page, tail=1)
+            first = max(0, kv - n - window + 1)  # the first token that is seen
+            table = table.copy()
+            table[0, : first // page] = -1 if back == "none" else cache[0].shape[0]
+            if back == "other":
+                spare = next(p for p in range(cache[0].shape[0]) if p not in table)
+                table[0, : first // page] = spare
+                cache[1][spare] = float("nan")
+                cache[3][spare] = float("nan")
+                zero = [t.clone() for t in cache]  # the reference multiplies by zero weights: finite values there
+                zero[1][spare] = 0
+                zero[3][spare] = 0
+                dev = [torch.from_numpy(np.ascontiguousarray(x)).cuda() for x in (cu, kvs, table)]
+                got = m.kv4_attention(q, cache, *dev, n, kv, window=window)
+                want, _ = check(m, q, zero, cu, kvs, table, 2, True, window, random=False)
+                assert torch.equal(got[: n + 1], want[: n + 1])
+            else:
+                check(m, q, cache, cu, kvs, table, 2, True, window, random=False)
+            m.check_status()
+    if back != "other":  # a page that is seen is still reported
+        table[0, first // page] = -1
+        check(m, q, cache, cu, kvs, table, 2, True, window, random=False)
+        assert m.get_status() == m.ERR_INDEX

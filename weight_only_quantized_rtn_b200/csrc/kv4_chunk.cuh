@@ -196,10 +196,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
     if (row0 >= rows) return;
 
     ChRange R[2];
-    int j0, j1;
+    int j0, j1, first_seen;
     {
         int lo, hi, unused;
         seen_range(a, kv - n + row0 / a.share, kv, lo, unused);
+        first_seen = lo;
         seen_range(a, kv - n + (min(rows, row0 + 2 * CH_ROWS) - 1) / a.share, kv, unused, hi);
         hi = min(hi, cover);
         const int u0 = lo / CH_KEYS, u1 = hi > 0 ? (hi - 1) / CH_KEYS + 1 : 0, units = max(0, u1 - u0);
@@ -458,7 +459,14 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
             }
         };
         pages(j0);
+        // the first step may begin behind the window, where pages may have been given back: its 16-token pieces before that
+        // of the first token seen are taken as no tokens
+        const int behind = (first_seen - j0 * CH_KEYS) & ~15;
+#pragma unroll
+        for (int r = 0; r < REP; ++r)
+            if (tk + r * TOK < behind) page[r] = -1;
         load(j0);
+        if (behind > 0) bad &= ~0u << (behind >> 4);
         pages(j0 + 1);
         for (int j = j0, it = 0; j < j1; ++j, ++it) {
             const int st = it & 1, ph = (it >> 1) & 1;

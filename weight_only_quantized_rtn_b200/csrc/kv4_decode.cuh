@@ -298,6 +298,8 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
     uint32_t pg[DEC_STAGES][2];  // pages of the units in flight, in order
 #pragma unroll
     for (int i = 0; i < DEC_STAGES; ++i) dec_pages(a, table, ub + warp + i * DEC_WARPS, ue, hi, pg[i]);
+    // the first tile may lie behind the window: its page may have been given back
+    if (ub + warp == u0 && lo >= u0 * DEC_UNIT + 16) pg[0][0] = 0xFFFFFFFFu;
 #pragma unroll
     for (int i = 0; i < DEC_STAGES - 1; ++i) {
         fetch(ub + warp + i * DEC_WARPS, pg[i], ring + i * R::STAGE);
@@ -387,7 +389,10 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
             const int tok0 = u * DEC_UNIT;
             const bool in0 = pg[0][0] < fetch.npages, in1 = pg[0][1] < fetch.npages;
             const bool inside = tok0 >= lo_all && tok0 + DEC_UNIT <= hi_all && in0 && in1;
-            if (!inside && ((!in0 && tok0 < hi) || (!in1 && tok0 + 16 < hi)) && lane == 0) raise_error(ERRBIT_INDEX);
+            if (!inside) {  // a page that some row sees a token of (the first row sees the earliest) must be there
+                const int first = __shfl_sync(0xffffffffu, clo[0][0], 0);
+                if (((!in0 && tok0 + 16 > first && tok0 < hi) || (!in1 && tok0 + 16 < hi)) && lane == 0) raise_error(ERRBIT_INDEX);
+            }
             float x[2][NT][4];
             uint32_t vs[2][2][(G + 1) / 2];
 #pragma unroll
