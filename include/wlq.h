@@ -390,7 +390,8 @@ wlq_status wlq_w4a4_linear(const void* x, int64_t M, const void* wq, const void*
  * q_out, k_out: bf16 with their own token strides; may be q and k themselves
  *          (same stride), otherwise they must not overlap any input
  * With a weight, values beyond 1e18 in magnitude, whose squares leave fp32,
- * are out of its range.
+ * are out of its range; small ones are not, whatever eps (a row of zeros with
+ * eps 0 is 0 / 0).
  * head_dim 64 or 128; rotary_dim a multiple of 16, at most head_dim; axes
  * 1..4; strides multiples of 8 and at least heads * head_dim; q, k, q_out and
  * k_out 16-byte aligned.  tokens == 0 is a no-op.

@@ -278,3 +278,38 @@ def test_two_streams_and_a_captured_append():
         m.kv4_append(want, x[:, :H], x[:, H:], cu, kv, table, T, pos, freq)
         assert all(torch.equal(a, b) for a, b in zip(want, got))
         assert all(torch.equal(a, b) for a, b in zip(back, m.kv4_read(want, cu, kv, table, T, T)))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("eps", [0.0, 1e-60, 1e-40, 1e-30])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rows_next_to_zero_are_normed(D, eps, inter):
+    """Rows whose squares leave fp32 below, beside ordinary ones in the same warp, with an eps too small to hide them."""
+    m = wlq()
+    T, H = 12, 5
+    x = _rows(D, T, H, D, 0.5).float()
+    for t, size in enumerate((1e-12, 1e-18, 1e-20, 1e-22, 1e-25, 1e-30, 1e-36, 1e-38, 4e-39)):
+        x[t, 1::2] *= size
+    x = x.bfloat16()
+    x[9, 2] = 0
+    x[9, 2, 7] = 9.2e-41          # one smallest subnormal among zeros
+    x[10, 3, 1:] *= 1e-25         # one ordinary value among tiny ones
+    if eps:
+        x[11, 0] = 0              # stays zero; with eps = 0 the formula is 0 / 0
+    w = (1 + 0.3 * _rows(3, 1, 1, D, 0.0).reshape(D)).bfloat16()
+    pos, freq = _positions(1, T, 1, 5000), _freq((D // 2,))
+    args = ref.f64(x), ref.f64(w), eps
+    o, k = m.qk_norm_rope(x.cuda(), x.cuda(), pos.cuda(), freq.cuda(), interleaved=inter, q_weight=w.cuda(), k_weight=w.cuda(), eps=eps)
+    _check_rows(ref.f64(o), *args, pos.numpy(), freq.numpy(), (D // 2,), inter)
+    assert torch.equal(o, k)
+    o, _ = m.qk_norm_rope(x.cuda(), None, q_weight=w.cuda(), eps=eps)
+    _check_rows(ref.f64(o), *args, None, None, None, True)
+    # the same rows into the cache: exact codes, nothing flagged
+    cu, kv, table = _dev(*_batch([T], [T], 16, 1)[:3])
+    cache = m.Kv4Cache(3, H, 16, D, 32)
+    m.kv4_append(cache, x.cuda(), x.cuda(), cu, kv, table, T, pos.cuda(), freq.cuda(), interleaved=inter, k_weight=w.cuda(), eps=eps)
+    m.check_status()
+    q, s = ref.quantize4(ref.key_bits(ref.norm_rope(*args, pos.numpy(), freq.numpy(), (D // 2,), inter)), 32)
+    p = int(table[0, 0])
+    np.testing.assert_array_equal(ref.unpack4(cache[0][p, :, :T].cpu().numpy().transpose(1, 0, 2), D), q)
+    np.testing.assert_array_equal(cache[1][p, :, :T].cpu().numpy().transpose(1, 0, 2).astype(np.float64), s)

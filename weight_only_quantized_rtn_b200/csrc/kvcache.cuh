@@ -19,7 +19,8 @@
 // within 5 * 2^-24 (squares exact, at most 7 additions of one-signed terms,
 // halved by the root; then the roundings of mean + eps and of the root), x w
 // is exact (8 + 8 bits), and there are three more roundings; then it is
-// rounded to bf16.
+// rounded to bf16.  Rows whose squares come near fp32's lower end are lifted
+// by a power of two first.
 //
 // The cache's codes are those of the REAL keys rounded to fp32 and from there
 // to bf16 (as a cast from a wider type rounds): a key on the other side of a
@@ -169,6 +170,9 @@ struct RopeLane {
 
 // A row's evaluation (8 values a lane): the products x w, the partners, the
 // results in fp32.
+// Rows whose mean square and eps leave little of fp32's range below them are
+// evaluated as x 2^100 and eps 2^200, which norm to the same values.
+constexpr float NORM_LOW = 7.888609052210118e-31f, NORM_UP = 1.2676506002282294e30f;  // 2^-100, 2^100
 struct RowEval {
     float2 x[4], p[4], y[4];
     float r;
@@ -185,7 +189,21 @@ __device__ __forceinline__ uint4 norm_rope_row(uint4 raw, const float2 (&w)[4], 
         float ss = q.x + q.y;
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        v.r = __frsqrt_rn(fmaf(ss, 1.0f / D, static_cast<float>(a.eps)));
+        float ms = fmaf(ss, 1.0f / D, static_cast<float>(a.eps));
+        if (__any_sync(0xffffffffu, ms < NORM_LOW)) {
+            const bool low = ms < NORM_LOW;
+            const float up = low ? NORM_UP : 1.0f;
+            ss = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v.x[i] = mul_f32x2(v.x[i], make_float2(up, up));
+                ss = fmaf(v.x[i].x, v.x[i].x, fmaf(v.x[i].y, v.x[i].y, ss));
+            }
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (low) ms = fmaf(ss, 1.0f / D, static_cast<float>(a.eps * NORM_UP * NORM_UP));
+        }
+        v.r = __frsqrt_rn(ms);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) v.x[i] = mul_f32x2(v.x[i], w[i]);  // exact: 8 x 8 bits
@@ -237,8 +255,9 @@ __device__ __forceinline__ bool settle_row(uint4 raw, bool norm, const RopeArgs&
 #pragma unroll
         for (int j = LPR / 2; j > 0; j >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, j);
         // two Newton steps from the fp32 root: 2^-22 -> 2^-43 -> fp64's own rounding
-        const double h = 0.5 * (ss / D + a.eps);
         r64 = static_cast<double>(v.r);
+        double h = 0.5 * (ss / D + a.eps);
+        if (h * r64 * r64 < 0.25) h *= static_cast<double>(NORM_UP) * NORM_UP;  // a lifted row (1/2 otherwise)
         r64 = r64 * fma(-h * r64, r64, 1.5);
         r64 = r64 * fma(-h * r64, r64, 1.5);
     }
