@@ -377,7 +377,7 @@ wlq_status wlq_w4a4_linear(const void* x, int64_t M, const void* wq, const void*
  *   each rotated pair (a, b), i = its number, angle = positions[t][axis(i)]
  *   * inv_freq[i]:   a' = a cos - b sin,  b' = a sin + b cos
  * evaluated in fp32 (within 9 * 2^-24 (|a| + |b|) of the real value, n's pair
- * (a, b); the angles in fp64, at any position) and rounded once to bf16.
+ * (a, b); the angles right to 2^-50 of a turn, at any position) and rounded once to bf16.
  * Pairs: interleaved != 0: inputs (2 i, 2 i + 1); 0: (i, i + rotary_dim / 2).
  * Inputs from rotary_dim on are normed but not rotated.  sections[a] pairs
  * turn by axis a, in order (1 axis: text; 2 or 3: height, width / time,

@@ -313,3 +313,64 @@ def test_rows_next_to_zero_are_normed(D, eps, inter):
     p = int(table[0, 0])
     np.testing.assert_array_equal(ref.unpack4(cache[0][p, :, :T].cpu().numpy().transpose(1, 0, 2), D), q)
     np.testing.assert_array_equal(cache[1][p, :, :T].cpu().numpy().transpose(1, 0, 2).astype(np.float64), s)
+
+
+def _exact_turn(pos, f):
+    """cos and sin of pos * f (both exact integers over powers of two), the angle reduced with 60 digits of pi."""
+    from decimal import Decimal, localcontext
+    with localcontext() as c:
+        c.prec = 90
+
+        def arctan_inverse(n):  # of 1 / n
+            x, total, k = Decimal(1) / n, Decimal(0), 0
+            while abs(x) > Decimal(10) ** -85:
+                total += x / (2 * k + 1) if k % 2 == 0 else -x / (2 * k + 1)
+                x /= n * n
+                k += 1
+            return total
+
+        two_pi = 8 * (4 * arctan_inverse(5) - arctan_inverse(239))  # Machin
+        a = Decimal(int(pos)) * Decimal(float(f))                   # exact: a float is a short decimal
+        a -= two_pi * (a / two_pi).to_integral_value()
+        return float(a)
+
+
+def _far_keys(seed, D, inter, group):
+    """Positions up to the ends of int32 and frequencies of full 24 bits: the angles have up to 55 bits.  Heads that hold one
+    pair of inputs, such that the exact rotation and that of the angle rounded to 53 bits round to different keys."""
+    g = np.random.default_rng(seed)
+    pairs = D // 2
+    freq = g.uniform(0.5, 1.0, pairs).astype(np.float32)
+    pos = np.array([(1 << 31) - 1, -(1 << 31) + 1, (1 << 31) - 3, (1 << 30) + 7, 1234567891, -1987654321, 2147400001, 2000000011], dtype=np.int64)
+    a, b = (t.ravel() for t in np.meshgrid(1 + np.arange(128) / 128, (1 + np.arange(128) / 128)[:, None] * np.array([-2, -1, 1, 2]), indexing="ij"))
+    rows = []
+    for t, p in enumerate(pos):
+        for i in range(0, pairs, 2):
+            w = [_exact_turn(p, freq[i]), _exact_turn(1, float(p) * float(freq[i]))]
+            first, second = ([f(u) for u in w] for f in (lambda u: a * np.cos(u) - b * np.sin(u), lambda u: a * np.sin(u) + b * np.cos(u)))
+            for y, other in ((first, second), (second, first)):
+                hit = (ref.key_bits(y[0]) != ref.key_bits(y[1])) & (np.abs(y[0]) > np.abs(other[0]))  # the largest of its group: the scale changes
+                rows += [(t, i, a[j], b[j], first[0][j], second[0][j]) for j in np.nonzero(hit)[0][:2]]
+    T, H = len(pos), len(rows)
+    x, y = np.zeros((T, H, D)), np.zeros((T, H, D))
+    for h, (t, i, a_, b_, f_, s_) in enumerate(rows):
+        at = [2 * i, 2 * i + 1] if inter else [i, i + pairs]
+        x[t, h, at], y[t, h, at] = (a_, b_), (f_, s_)
+    return pos.astype(np.int32), freq, x, *ref.quantize4(ref.key_bits(y), group)
+
+
+@pytest.mark.parametrize("D,inter", [(128, True), (64, False)])
+def test_append_at_the_ends_of_the_positions(D, inter):
+    m = wlq()
+    group = 32
+    pos, freq, x, q, s = _far_keys(D, D, inter, group)
+    T, H = x.shape[:2]
+    assert H >= 12
+    k = torch.from_numpy(x).bfloat16().cuda()
+    cu, kv, table = _dev(*_batch([T], [T], 16, 1)[:3])
+    cache = m.Kv4Cache(3, H, 16, D, group)
+    m.kv4_append(cache, k, k, cu, kv, table, T, torch.from_numpy(pos).cuda(), torch.from_numpy(freq).cuda(), interleaved=inter)
+    m.check_status()
+    p = int(table[0, 0])
+    np.testing.assert_array_equal(ref.unpack4(cache[0][p, :, :T].cpu().numpy().transpose(1, 0, 2), D), q)
+    np.testing.assert_array_equal(cache[1][p, :, :T].cpu().numpy().transpose(1, 0, 2).astype(np.float64), s)

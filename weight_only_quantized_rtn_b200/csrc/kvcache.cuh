@@ -123,11 +123,12 @@ __device__ __forceinline__ void token_turns(const RopeArgs& a, int64_t token, To
 #pragma unroll
         for (int k = 0; k < ROPE_MAX_AXES - 1; ++k)
             if (k + 1 < a.axes && i >= a.sec_end[k]) ax = k + 1;
-        // the angle has at most 31 + 24 bits; 1 / (2 pi) as a sum of two doubles keeps its turns to
-        // about 2^-53 at any position
-        const double angle = static_cast<double>(a.pos[token * a.axes + ax]) * static_cast<double>(a.inv_freq[i]);
+        // the angle has up to 32 + 24 bits: the product and what its rounding left off; 1 / (2 pi) as a sum
+        // of two doubles.  The turns are then right to about 2^-53 at any position.
+        const double pos = static_cast<double>(a.pos[token * a.axes + ax]), freq = static_cast<double>(a.inv_freq[i]);
+        const double angle = pos * freq, off = fma(pos, freq, -angle);
         const double t = angle * 0.15915494309189535;
-        const double rest = fma(angle, -9.839338337591243e-18, fma(angle, 0.15915494309189535, -t));
+        const double rest = fma(angle, -9.839338337591243e-18, fma(angle, 0.15915494309189535, -t)) + off * 0.15915494309189535;
         double c, s;
         sincospi(2.0 * ((t - rint(t)) + rest), &s, &c);
         T.d[i] = make_double2(c, s);
