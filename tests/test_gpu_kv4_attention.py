@@ -407,3 +407,25 @@ def test_pages_given_back_behind_the_window(D, group, page, n, share, back):
         table[0, first // page] = -1
         check(m, q, cache, cu, kvs, table, 2, True, window, random=False)
         assert m.get_status() == m.ERR_INDEX
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_a_sequence_of_as_many_tokens_as_a_length_holds(n):
+    """2^31 - 1 cached tokens (one page over and over, another at the end): the place after the last token is not one."""
+    m = wlq()
+    D, page, kv = 64, 256, (1 << 31) - 1
+    cache = m.Kv4Cache(2, 1, page, D, 64)
+    cache[0].fill_(0x11)                     # the same low score for every token (a place without one would have 0)
+    cache[1].fill_(1.0)
+    cache[2].fill_(0x99)                     # values of one
+    cache[3].fill_(1.0)
+    cache[1][1, :, -1] = float("nan")        # what no token was written to
+    cache[3][1, :, -1] = float("nan")
+    cache[2][1, :, -1] = 0
+    table = torch.zeros(1, 1 << 23, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    q = torch.ones(n, 1, D, dtype=torch.bfloat16, device="cuda")
+    cu, kvs = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, n], [kv]))
+    o = m.kv4_attention(q, cache, cu, kvs, table, n, kv, causal=False)
+    m.check_status()
+    assert (o == 1).all()                    # sums of ones: exact, each accumulator has less than 2^24 of them (or steps of 16)

@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) kv4_chunk_kernel(const AttnArgs
             // the step's slot is written again four steps later, when this tile's weights have been used
             const uint4 bad4 = *reinterpret_cast<const uint4*>(pbad + (j & 3) * 4);
             const uint32_t bad = bad4.x | bad4.y | bad4.z | bad4.w;
-            const bool inside = __all_sync(0xffffffffu, k0 >= lo && k0 + CH_KEYS <= hi && bad == 0);
+            const bool inside = __all_sync(0xffffffffu, k0 >= lo && k0 <= hi - CH_KEYS && bad == 0);
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 uint32_t v[4][16];

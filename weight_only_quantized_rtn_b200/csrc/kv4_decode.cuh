@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, NT == 1 ? 4 : 3) kv4_decode_ke
             const uint8_t* sc = dec_smem + (sk - smem_u32(dec_smem)) + 2 * R::CODES;
             const int tok0 = u * DEC_UNIT;
             const bool in0 = pg[0][0] < fetch.npages, in1 = pg[0][1] < fetch.npages;
-            const bool inside = tok0 >= lo_all && tok0 + DEC_UNIT <= hi_all && in0 && in1;
+            const bool inside = tok0 >= lo_all && tok0 <= hi_all - DEC_UNIT && in0 && in1;  // (tok0 + 32 may leave 32 bits)
             if (!inside) {  // a page that some row sees a token of (the first row sees the earliest) must be there
                 const int first = __shfl_sync(0xffffffffu, clo[0][0], 0);
                 if (((!in0 && tok0 + 16 > first && tok0 < hi) || (!in1 && tok0 + 16 < hi)) && lane == 0) raise_error(ERRBIT_INDEX);
