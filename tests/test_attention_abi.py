@@ -159,3 +159,13 @@ def test_caches_copy_and_save():
     cache = m.Kv4Cache(3, 2, 16, 64, 32, device="cpu")
     for again in (copy.copy(cache), copy.deepcopy(cache), pickle.loads(pickle.dumps(cache))):
         assert [(t.shape, t.dtype) for t in again] == [(t.shape, t.dtype) for t in cache]
+
+
+def test_every_status_has_its_name():
+    import os
+    import re
+
+    header = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(m.__file__))), "include", "wlq.h")).read()
+    names = {int(v): n for n, v in re.findall(r"(WLQ_(?:OK|ERR_\w+)) = (\d+)", header)}
+    assert names == m.STATUS_NAMES
+    assert "WLQ_ERR_INDEX" in str(m.WlqError(m.ERR_INDEX, "x"))

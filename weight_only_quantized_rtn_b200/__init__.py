@@ -23,7 +23,7 @@ STATUS_NAMES = {
     OK: "WLQ_OK", ERR_INVALID_ARG: "WLQ_ERR_INVALID_ARG", ERR_SHAPE: "WLQ_ERR_SHAPE",
     ERR_ALIGN: "WLQ_ERR_ALIGN", ERR_UNSUPPORTED: "WLQ_ERR_UNSUPPORTED",
     ERR_NONFINITE: "WLQ_ERR_NONFINITE", ERR_WORKSPACE: "WLQ_ERR_WORKSPACE",
-    ERR_TIMEOUT: "WLQ_ERR_TIMEOUT", ERR_CUDA: "WLQ_ERR_CUDA",
+    ERR_TIMEOUT: "WLQ_ERR_TIMEOUT", ERR_CUDA: "WLQ_ERR_CUDA", ERR_INDEX: "WLQ_ERR_INDEX",
 }
 EXPORTS = ("wlq_quantize", "wlq_quantize_pack", "wlq_quantize_ex", "wlq_quantize_fp8", "wlq_packed_bytes",
            "wlq_pack", "wlq_unpack", "wlq_linear_workspace", "wlq_linear", "wlq_linear_noalloc",
