@@ -468,14 +468,14 @@ wlq_status wlq_kv4_read(const int32_t* cu_seqlens, const int32_t* kv_lens, int b
  * max_kv: an upper bound of kv_lens (host).  It only plans how long caches are
  *         split; any value gives right results.  Tokens of a page out of range
  *         and tokens past the table count as not seen (WLQ_ERR_INDEX is set).
- * scale: finite, any sign.  Scores, softmax statistics and sums are fp32, the
- * inputs of the tensor cores fp16, each rounded once: queries as q 2^e with one
- * power of two per row (exact unless a value lies 2^-29 below its row's
- * largest); at most 32 rows (queries x q_heads / kv_heads) of a sequence: keys
- * and values as their codes (exact), weights as exp(. - max) times the value's
- * scale (off by 2^-11 of it, or 2^-25 of the largest such product that the row
- * and group have seen); more rows: keys and values as code * scale, weights as
- * exp(. - max) (off by 2^-11, or 2^-25 of the largest weight).
+ * scale: at most 2e38 in magnitude, any sign.  Scores, softmax statistics and
+ * sums are fp32, the inputs of the tensor cores fp16, each rounded once: queries
+ * as q 2^e with one power of two per row (exact unless a value lies 2^-29 below
+ * its row's largest); at most 32 rows (queries x q_heads / kv_heads) of a
+ * sequence: keys and values as their codes (exact), weights as exp(. - max)
+ * times the value's scale (off by 2^-11 of it, or 2^-25 of the largest such
+ * product that the row and group have seen); more rows: keys and values as
+ * code * scale, weights as exp(. - max) (off by 2^-11, or 2^-25 of the largest).
  * Results are bitwise reproducible run to run.
  * workspace: wlq_kv4_attention_workspace() bytes (0: none needed), 16-byte
  * aligned, contents need no initialisation; calls that may overlap on the GPU

@@ -169,3 +169,8 @@ def test_every_status_has_its_name():
     names = {int(v): n for n, v in re.findall(r"(WLQ_(?:OK|ERR_\w+)) = (\d+)", header)}
     assert names == m.STATUS_NAMES
     assert "WLQ_ERR_INDEX" in str(m.WlqError(m.ERR_INDEX, "x"))
+
+
+@pytest.mark.parametrize("scale", [2.1e38, -3.4e38])
+def test_scales_whose_power_of_two_form_leaves_fp32_are_refused(scale):
+    assert attend(scale=scale) == m.ERR_INVALID_ARG

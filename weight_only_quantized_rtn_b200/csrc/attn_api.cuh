@@ -365,7 +365,7 @@ wlq_status wlq_kv4_attention(const void* q, int64_t q_stride, int64_t tokens, in
     if ((st = check_pool(k_codes, k_scales, v_codes, v_scales, num_pages, page_size, group, kv_heads, head_dim, &a.P)) != WLQ_OK)
         return st;
     if (max_kv < 0) return fail(WLQ_ERR_INVALID_ARG, "max_kv must be >= 0");
-    if (!std::isfinite(scale)) return fail(WLQ_ERR_INVALID_ARG, "scale must be finite");
+    if (!(std::fabs(scale) <= 2e38f)) return fail(WLQ_ERR_INVALID_ARG, "scale must be finite, at most 2e38 in magnitude");  // times log2(e): fp32
     if (window < 0 || (window > 0 && !causal)) return fail(WLQ_ERR_INVALID_ARG, "a window needs causal and must be >= 0");
     if (static_cast<int64_t>(max_q) * (q_heads / kv_heads) >= (int64_t(1) << 31))
         return fail(WLQ_ERR_SHAPE, "max_q * q_heads / kv_heads must stay below 2^31");
