@@ -174,3 +174,9 @@ def test_every_status_has_its_name():
 @pytest.mark.parametrize("scale", [2.1e38, -3.4e38])
 def test_scales_whose_power_of_two_form_leaves_fp32_are_refused(scale):
     assert attend(scale=scale) == m.ERR_INVALID_ARG
+
+
+def test_a_bound_beyond_every_length_plans_like_the_largest_length():
+    f = m.kv4_attention_workspace
+    for rows in (1, 64):
+        assert f(rows, 1, rows, (1 << 63) - 1, 8, 8, 128) == f(rows, 1, rows, 1 << 31, 8, 8, 128) > 0

@@ -130,7 +130,7 @@ DecPlan dec_plan(int64_t tokens, int batch, int max_q, int64_t max_kv, int q_hea
     p.chunk = rows > 32;
     p.nt = rows > 8 ? 2 : 1;
     p.row_tiles = static_cast<int>(cdiv(rows, p.chunk ? 2 * wlq::CH_ROWS : 8 * p.nt));
-    int64_t seen = std::max<int64_t>(max_kv, 1);
+    int64_t seen = std::min(std::max<int64_t>(max_kv, 1), int64_t(1) << 31);  // a bound beyond what a length can be is none
     if (window > 0) seen = std::min<int64_t>(seen, static_cast<int64_t>(window) + max_q);
     const int64_t base = static_cast<int64_t>(batch) * kv_heads * p.row_tiles;
     const int64_t units = cdiv(seen, p.chunk ? wlq::CH_KEYS : wlq::DEC_UNIT);
