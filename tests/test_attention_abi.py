@@ -180,3 +180,24 @@ def test_a_bound_beyond_every_length_plans_like_the_largest_length():
     f = m.kv4_attention_workspace
     for rows in (1, 64):
         assert f(rows, 1, rows, (1 << 63) - 1, 8, 8, 128) == f(rows, 1, rows, 1 << 31, 8, 8, 128) > 0
+
+
+@pytest.mark.parametrize("name,kw", [("max_q", dict(max_q=(1 << 32) + 1)), ("max_q", dict(max_q=-1)), ("window", dict(window=(1 << 32) + 3)),
+                                     ("window", dict(window=-(1 << 32)))])
+def test_bounds_that_32_bits_do_not_hold_are_refused(name, kw, monkeypatch):
+    """They would reach the library as their lower 32 bits."""
+    import torch
+
+    monkeypatch.setattr(m, "_on", lambda *a: None)
+    cache = m.Kv4Cache(3, 2, 16, 64, 32, device="cpu")
+    i32 = [torch.zeros(n, dtype=torch.int32) for n in (2, 1)] + [torch.zeros(1, 3, dtype=torch.int32)]
+    a = dict(max_q=1, max_kv=4)
+    a.update(kw)
+    q = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(m.WlqError, match=name):
+        m.kv4_attention(q, cache, *i32, **a)
+    if name == "max_q":
+        with pytest.raises(m.WlqError, match=name):
+            m.kv4_append(cache, q, q, *i32, a["max_q"])
+        with pytest.raises(m.WlqError, match=name):
+            m.kv4_read(cache, *i32, a["max_q"], 1)

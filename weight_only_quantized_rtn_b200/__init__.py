@@ -466,6 +466,8 @@ def _batch(cu_seqlens, kv_lens, block_table, max_q: int):
     if (cu_seqlens.dtype is not i32 or kv_lens.dtype is not i32 or block_table.dtype is not i32 or cu_seqlens.numel() != n + 1
             or kv_lens.numel() != n or not (cu_seqlens.is_contiguous() and kv_lens.is_contiguous() and block_table.is_contiguous())):
         raise WlqError(ERR_INVALID_ARG, "contiguous int32 cu_seqlens [batch + 1], kv_lens [batch], block_table [batch, width]")
+    if max_q >> 31:  # ctypes would pass its lower 32 bits
+        raise WlqError(ERR_INVALID_ARG, "max_q must be 0 .. 2^31 - 1")
     return cu_seqlens.data_ptr(), kv_lens.data_ptr(), n, max_q, block_table.data_ptr(), width
 
 
@@ -538,6 +540,8 @@ def kv4_attention(q, cache, cu_seqlens, kv_lens, block_table, max_q: int, max_kv
     _want(lse is None or (lse.shape == (T, Hq) and lse.dtype is torch.float32 and lse.is_contiguous()),
           "lse must be contiguous fp32 [tokens, q_heads]")
     batch = _batch(cu_seqlens, kv_lens, block_table, max_q)
+    if window >> 31:
+        raise WlqError(ERR_INVALID_ARG, "window must be 0 .. 2^31 - 1")
     if workspace is None:
         n = int(lib.wlq_kv4_attention_workspace(T, batch[2], batch[3], max_kv, Hq, H, D))
         workspace = out.new_empty((n + 1) // 2) if n else None  # bf16: two bytes each
