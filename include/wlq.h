@@ -296,8 +296,8 @@ wlq_status wlq_lowrank_residual(const float* W, const void* L1, const void* L2, 
 
 /*
  * Synchronise `stream`, then read and clear this device's error word:
- * WLQ_OK, WLQ_ERR_NONFINITE, WLQ_ERR_TIMEOUT or WLQ_ERR_INDEX (or
- * WLQ_ERR_CUDA).
+ * WLQ_OK, WLQ_ERR_TIMEOUT, WLQ_ERR_NONFINITE or WLQ_ERR_INDEX (or
+ * WLQ_ERR_CUDA); where several happened, the first of these in that order.
  * The error path follows "Nunchaku Lite", section "hardware and precision
  * support": the quantizer checks the GPU's compute capability when it loads
  * and raises a clear error on a mismatch.  Here every call returns

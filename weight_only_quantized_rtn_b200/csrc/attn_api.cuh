@@ -126,7 +126,8 @@ DecPlan dec_plan(int64_t tokens, int batch, int max_q, int64_t max_kv, int q_hea
     DecPlan p;
     const int64_t rows = static_cast<int64_t>(max_q) * (q_heads / kv_heads);
     // Up to 32 rows the few-row kernel, which reads the cache once for each 16 (8 sequences of 8192, 1 of 32768, 32 of
-    // 1500 tokens, D = 128: 45, 41, 44 us against 75, 43, 55 by the chunk kernel; 48 rows: 66, 53, 60 against 77, 44, 55).
+    // 1500 tokens, 8 cache heads, D = 128, groups of 64: 71, 41, 59 us against 77, 47, 62 by the chunk kernel; 48 rows: 104,
+    // 53, 86 against 77, 48, 63).
     p.chunk = rows > 32;
     p.nt = rows > 8 ? 2 : 1;
     p.row_tiles = static_cast<int>(cdiv(rows, p.chunk ? 2 * wlq::CH_ROWS : 8 * p.nt));

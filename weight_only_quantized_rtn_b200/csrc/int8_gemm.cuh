@@ -14,7 +14,9 @@
 //    complete on the first CTA's barrier, whose thread issues the MMAs.  Per
 //    SM and stage that is 32 KB for 512 clocks of MMAs; a single CTA with the
 //    same tile would need 48 KB.  bn is chosen so that the token tiles are
-//    even and the last round of tiles is as full as can be.
+//    even and the last round of tiles is as full as can be; over the shapes
+//    timed (1560 x 16384 x 4096: 75.0 to 75.5 us for every bn from 128 to 256)
+//    it hardly matters.
 //  - single CTAs otherwise, 128 channels x bn tokens, K split over the S CTAs
 //    of a cluster when there are few tiles: the integer partial sums are added
 //    through distributed shared memory, in any order the same.
@@ -25,11 +27,14 @@
 // lane's divergent code the same tiles took 134 us instead of 87 (1560 x 16384
 // x 4096).
 //
-// Bound: the tensor pipe for many tokens (6240 x 4096 x 16384: 264 us, 3.2
-// POP/s, twice the bf16 rate; 1560 x 16384 x 4096: 77 us, its 448 tiles filling
-// 6.05 of 7 rounds), the weights' bytes and the launch for few (16 x 4096 x
-// 4096: 6.9 us back to back).  quantize_tokens_kernel: HBM (6240 x 16384: 60 us
-// for 306 MB).
+// Bound: the tensor pipe and the power cap for many tokens (back to back 6240 x
+// 4096 x 16384: 273 us, 3.07 POP/s, single launches 264; 1560 x 16384 x 4096:
+// 75 us, 2.79 POP/s, twice the sustained bf16 rate, the tensor pipe 72 % active
+// and 8.65 of its 9 rounds of tiles filled; the weights pass once for each of
+// its ten token tiles and leave L2 on the way: 141 MB read from DRAM where the
+// operands have 73), the weights' bytes and the launch for few (16 x 4096 x 4096:
+// 6.9 us back to back).  quantize_tokens_kernel: HBM (6240 x 16384: 60 us for
+// 306 MB).
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>

@@ -16,7 +16,10 @@
 // K and V tiles are written by the dequantisation warps as fp16 code * scale
 // (one rounding) in one layout: rows of 64 inputs (128 bytes, 128-byte
 // swizzle), which is the K-major operand of the scores and the MN-major operand
-// of the outputs.  A lane takes 16 bytes of codes (32 inputs, one scale); the
+// of the outputs.  (Exact codes would want their scales on the scores, one more
+// multiplication each in the warps that set the pace, and on the weights; the
+// rounding and that of the weights leave 0.00172 of the result's 2-norm where
+// bf16's own output rounding leaves 0.00166.)  A lane takes 16 bytes of codes (32 inputs, one scale); the
 // order in which it stores its four 16-byte results alternates with the
 // row half, so a quarter warp's stores cover all banks.
 //
@@ -28,7 +31,7 @@
 // Bound: the exponentials (16 a clock and SM) and the tensor cores, which take
 // the same time for D = 128: 4 x 512 clocks of MMAs and 2 x 1024 of
 // exponentials for 256 rows x 128 tokens.  Measured: 1560 queries over 7800
-// tokens, 32 heads, 286 us (697 TFLOP/s; 298 before the 76 of its 224 row tiles
+// tokens, 32 heads, 288 us (691 TFLOP/s; 298 before the 76 of its 224 row tiles
 // that a second round of 148 CTAs took were split; 4300 clocks a step, tensor
 // pipe 34 % active, exponentials 40 %).  One warpgroup for keys and values took 424 us,
 // weights handed over whole 352; 64-column score buffers used in turn, so that

@@ -22,7 +22,7 @@
 //    of THIS row and group between 2^6 and 2^15.  Otherwise one token or group
 //    with large values, seen or not, would cost all others their bits.  The
 //    factors lie in shared memory; with them alone (no common reference) 64
-//    ragged sequences took 120 us against 107, two long ones 88 against 73.
+//    ragged sequences took 120 us against 111, two long ones 88 against 74.
 // ldmatrix hands a lane word t of 16 bytes of row g (K), and with .trans the
 // 16-bit pieces of two tokens side by side (V): four inputs of a token pair,
 // one mask-or and one exact fp16 operation from the MMA's operand.  P^T moves
@@ -38,14 +38,18 @@
 // parts by their cluster through distributed shared memory, others by
 // kv4_combine_kernel.
 //
-// Bound: HBM (each cached byte once); next to it the integer pipe, which takes
-// the codes apart (some 600 instructions a warp for 32 tokens of D = 128, where
-// HBM's rate leaves 700 issue slots).  Measured: 64 sequences of up to 8191
-// tokens, 368 MB, 109 us (3.4 TB/s, 0.51 of the copy rate; issue 65 % active);
-// two of up to 131072, 262 MB, 73 us.  Scales on the codes and register
-// prefetch took 207 and 136 us.  Feeding K's stored nibbles without their exact
-// subtraction (the offsets' sum taken off the scores) left the integer work as
-// it is and was no faster.
+// Bound: none at its limit.  A warp issues 765 instructions for 32 tokens of
+// D = 128 (745 before the scales were watched), as many as there are issue
+// slots at HBM's rate (748), and with 15 of the 16 warps that fit an SM
+// resident issue is 65 % active, the integer pipe, which takes the codes apart,
+// 53 %.  Measured: 64 sequences of up to 8191 tokens, 368 MB, 109 us (3.4 TB/s,
+// 0.51 of the copy rate); two of up to 131072, 262 MB, 73 us.  Where scales lie
+// too far apart for the common reference 126 and 84 us.  Scales on the codes
+// and register prefetch took 207 and 136 us.  Feeding K's stored nibbles without
+// their exact subtraction (the offsets' sum taken off the scores) left the
+// integer work as it is and was no faster.  Registers spilled a thread, of
+// D = 128: 8 to 24 bytes for up to 8 rows in groups of 64 and 32, 68 to 256
+// bytes for 16 rows.
 #pragma once
 #include <cstdint>
 #include <type_traits>

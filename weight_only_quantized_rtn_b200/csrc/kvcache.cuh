@@ -37,8 +37,9 @@
 // shuffle reduction and the half-split partner one shuffle.  A CTA works out
 // its token's angles once, in fp64, and walks the token's heads with cos and
 // sin in registers.  Measured for 6240 tokens: norm + rotation of 64 heads 45 us
-// (205 MB: 0.69 of the copy rate; issue 66 % active), append of 32 heads 73 us
-// (120 MB; issue 73 % active: the exact rounding), read back 28 us (122 MB).
+// (205 MB: 0.69 of the copy rate; issue 69 % active, half of the warps that fit
+// resident), append of 32 heads 77 us (129 MB; issue 74 % active: norm, rotation
+// and the exact rounding of the keys), read back 28 us (129 MB).
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
